@@ -361,6 +361,117 @@ LLMINT8_API llmint8_status_t llmint8_matmul_e4m3(const uint16_t *X, int64_t T, i
                                                  uint16_t *out, void *ws, size_t ws_bytes,
                                                  hipStream_t stream);
 
+/*
+ * Block-scaled FP8.  The decomposition above keeps an outlier column from
+ * spoiling the scale of its rows by taking it out in fp16; a scale for every
+ * block of 128 columns confines it to its block instead, so that activations
+ * are quantized once, by whatever produces them, and the product has one part.
+ *
+ * Operands are E4M3 codes with one power-of-two scale per block: 1 x 128 (a
+ * row of activations) or 128 x 128 (a weight).  The convention is that of the
+ * _e4m3 functions, per block: for a block with largest magnitude a,
+ *
+ *   e     = largest integer with a * 2^e <= 448, at most 126   (0 for a = 0)
+ *   code  = E4M3 nearest to x * 2^e, ties to even
+ *   scale = E8M0 byte 127 - e, which stands for 2^-e
+ *
+ * A block that holds an infinity or a NaN has the scale byte 255 (NaN) and
+ * NaN codes, and makes every output that it enters NaN.  Scale matrices have
+ * rows of llmint8_b128_pitch(K) bytes: one per block of 128 columns, padded
+ * to a multiple of 4 with 127.  SX is [T, pitch], SB is [ceil(N/128), pitch]
+ * (per expert).  K and N are multiples of 64, so the last block may be 64 wide.
+ * K <= 133144, N <= 2^24, rows <= 2^31 - 2^16, at most 1024 experts, at most
+ * 2^38 outputs of a product; beyond these -> LLMINT8_ERR_UNSUPPORTED_SHAPE.
+ *
+ * 16-bit inputs and outputs are fp16 or bf16 (`type`).  Scale matrices,
+ * offsets and indices are 4-byte aligned, the optional bias 8-byte, all else
+ * 16-byte; conventions are otherwise those at the top of this file.
+ */
+enum { LLMINT8_F16 = 0, LLMINT8_BF16 = 1 };
+
+/* Bytes per row of a scale matrix: ceil(K/128) rounded up to 4; 0 for K <= 0. */
+LLMINT8_API int64_t llmint8_b128_pitch(int64_t K);
+
+/*
+ * RMS norm with the residual's addition and an output in 8 bits:
+ *
+ *   h[t,k] = X[t,k] + residual[t,k], rounded to `type`       (X without residual)
+ *   y[t,k] = h[t,k] / sqrt(mean_k(h[t,k]^2) + eps) * gamma[k] (fp32)
+ *
+ * Xq8 [T,K] and SX [T,pitch] are the codes and scales of y (of the fp32 values:
+ * one rounding).
+ *   X, residual in : [T,K], residual may be NULL
+ *   gamma       in : [K]
+ *   eps         in : finite, >= 0
+ *   residual_out   : NULL, or [T,K] out: h (requires residual); may be residual
+ *                    or X itself (in place), not a shifted part of them
+ *   Y              : NULL, or [T,K] out: y rounded to `type`, e.g. for a router;
+ *                    may be X or residual itself, but not residual_out
+ * The sum of squares is formed in fp32.
+ */
+LLMINT8_API llmint8_status_t llmint8_rmsnorm_b128(const uint16_t *X, const uint16_t *residual,
+                                                  const uint16_t *gamma, int type, int64_t T,
+                                                  int64_t K, float eps, uint8_t *Xq8, uint8_t *SX,
+                                                  uint16_t *residual_out, uint16_t *Y,
+                                                  hipStream_t stream);
+
+/* Activation quantization in blocks of 1 x 128: X [T,K] -> Xq8 [T,K], SX [T,pitch]. */
+LLMINT8_API llmint8_status_t llmint8_quantize_act_b128(const uint16_t *X, int type, int64_t T,
+                                                       int64_t K, uint8_t *Xq8, uint8_t *SX,
+                                                       hipStream_t stream);
+
+/* Weight quantization in blocks of 128 x 128, once per weight, of E stacked
+ * weights (E = 1: a single one): W_t [E,N,K] -> CB8 [E,N,K],
+ * SB [E,ceil(N/128),pitch]. */
+LLMINT8_API llmint8_status_t llmint8_quantize_weight_b128(const uint16_t *W_t, int type, int64_t E,
+                                                          int64_t K, int64_t N, uint8_t *CB8,
+                                                          uint8_t *SB, hipStream_t stream);
+
+/* Bytes of workspace llmint8_matmul_b128 needs (0: none, ws may be NULL); 0
+ * for invalid sizes. */
+LLMINT8_API size_t llmint8_matmul_b128_workspace_bytes(int64_t T, int64_t K, int64_t N);
+
+/*
+ * The product of block-scaled operands:
+ *
+ *   out[t,n] = act( sum_k x(t,k) * w(n,k) [+ bias[n]] ), rounded to `type`
+ *
+ * with x(t,k) = e4m3(Xq8[t,k]) * 2^(SX[t,k/128] - 127) and
+ * w(n,k) = e4m3(CB8[n,k]) * 2^(SB[n/128,k/128] - 127).  The scaled products are
+ * summed in fp32 by v_mfma_scale_f32_*_f8f6f4 (sums as described for the FP8
+ * variant above).  bias [N] or NULL is of `type`; activation as for
+ * llmint8_matmul_act.
+ */
+LLMINT8_API llmint8_status_t llmint8_matmul_b128(const uint8_t *Xq8, const uint8_t *SX, int64_t T,
+                                                 int64_t K, int64_t N, const uint8_t *CB8,
+                                                 const uint8_t *SB, const uint16_t *bias,
+                                                 int activation, int type, uint16_t *out,
+                                                 void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The products of E experts with ragged row counts: for i in
+ * [offsets[e], offsets[e+1])
+ *
+ *   out[i,n] = act( sum_k x(t,k) * w(e,n,k) [+ bias[e,n]] ),  t = row_idx ? row_idx[i] : i
+ *
+ *   Xq8, SX  in : [T,K], [T,pitch]
+ *   CB8, SB  in : [E,N,K], [E,ceil(N/128),pitch]
+ *   offsets  in : int32 [E+1] on the device, non-decreasing, within [0, M]
+ *   row_idx  in : int32 [M] on the device, each in [0, T), any order and repeated
+ *                 as often as needed; NULL: row i of Xq8 (then M = T)
+ *   bias     in : [E,N] or NULL
+ *   out     out : [M,N]; rows outside [offsets[0], offsets[E]) are left as they were
+ *
+ * The group sizes stay on the device: nothing is copied to the host.  Offsets
+ * outside [0, M] and indices outside [0, T) are taken as the nearest bound
+ * (no access leaves the arrays); decreasing offsets give unspecified rows.
+ * With row_idx, T * K < 2^32 (else LLMINT8_ERR_UNSUPPORTED_SHAPE).
+ */
+LLMINT8_API llmint8_status_t llmint8_matmul_grouped_b128(
+    const uint8_t *Xq8, const uint8_t *SX, int64_t T, int64_t K, int64_t N, const uint8_t *CB8,
+    const uint8_t *SB, int64_t E, const int32_t *offsets, const int32_t *row_idx, int64_t M,
+    const uint16_t *bias, int activation, int type, uint16_t *out, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

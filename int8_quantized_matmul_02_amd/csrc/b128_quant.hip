@@ -1,0 +1,365 @@
+// b128_quant.hip -- block-scaled FP8 quantization: the RMS norm with residual
+// addition and 8-bit output, the activation quantizer (1 x 128 blocks) and the
+// weight quantizer (128 x 128 blocks).  All three stream: each input byte is
+// read once and each output byte written once, so HBM bounds them at large
+// sizes and the launch at small ones.
+#include "b128.h"
+
+namespace llmint8 {
+namespace {   // internal linkage: nothing here is exported from the library
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ unsigned umax(unsigned a, unsigned b) { return a > b ? a : b; }
+
+// Max of v over each group of 2^n consecutive lanes.
+template <int kLanes>
+__device__ __forceinline__ unsigned group_max(unsigned v)
+{
+#pragma unroll
+    for (int off = 1; off < kLanes; off *= 2)
+        v = umax(v, (unsigned)__shfl_xor((int)v, off, kWave));
+    return v;
+}
+
+__device__ __forceinline__ unsigned word(uint4 v, int i)
+{
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ uint16_t elem(uint4 v, int i)
+{
+    const unsigned w = word(v, i / 2);
+    return (uint16_t)(i & 1 ? w >> 16 : w & 0xffffu);
+}
+template <int kT>
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        f[i] = t2f<kT>(elem(v, i));
+}
+template <int kT>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+{
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = (unsigned)f2t<kT>(f[2 * i]) | ((unsigned)f2t<kT>(f[2 * i + 1]) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Largest magnitude of 8 16-bit elements, as their 15 magnitude bits: these
+// order like the magnitudes in both types, with infinities and NaN above all
+// finite values, so an integer maximum also finds those.
+__device__ __forceinline__ unsigned absmax8(uint4 v)
+{
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const unsigned w = word(v, i);
+        m = umax(m, umax(w & 0x7fffu, (w >> 16) & 0x7fffu));
+    }
+    return m;
+}
+template <int kT>
+__device__ __forceinline__ unsigned mag_bits_f32(unsigned m)
+{
+    return __builtin_bit_cast(unsigned, t2f<kT>((uint16_t)m));
+}
+
+template <int kT>
+__device__ __forceinline__ uint2 quant8_b128(uint4 v, float mul)
+{
+    float f[8];
+    unpack8<kT>(v, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        f[i] *= mul;
+    return cvt8_e4m3(f);
+}
+
+// ---------------------------------------------------------------------------
+// RMS norm: TPR threads hold one row in registers as its 16-bit values (h is
+// rounded to the element type before anything else reads it, so 16 bits hold
+// it exactly), NC chunks of 8 elements each; chunk c belongs to thread
+// c % TPR, so 16 consecutive lanes hold one block of 128 and find its largest
+// magnitude by lane exchanges.  One pass over memory: sums of squares, the
+// normalized values and their codes all come from the registers.
+// ---------------------------------------------------------------------------
+template <int kT, int TPR, int NC>
+__global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void k_rmsnorm_b128(RmsNormArgs a,
+                                                                                int pitch)
+{
+    constexpr int kRows = TPR < kThreads ? kThreads / TPR : 1;   // rows per block
+    const int tid = threadIdx.x % TPR;
+    const int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+    const bool live = t < a.T;   // a wavefront without a row still meets the barrier
+    const int64_t row = live ? t : a.T - 1;
+    const int nchunk = (int)(a.K / 8);
+    const uint4 *x = reinterpret_cast<const uint4 *>(a.X + row * a.K);
+    const uint4 *r = reinterpret_cast<const uint4 *>(a.R ? a.R + row * a.K : a.X);
+    const uint4 *g = reinterpret_cast<const uint4 *>(a.G);
+
+    uint4 h[NC], gm[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int c = tid + j * TPR;
+        h[j] = c < nchunk ? x[c] : make_uint4(0, 0, 0, 0);
+    }
+    if (a.R) {
+        uint4 rr[NC];
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const int c = tid + j * TPR;
+            rr[j] = c < nchunk ? r[c] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            float p[8], q[8];
+            unpack8<kT>(h[j], p);
+            unpack8<kT>(rr[j], q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                p[i] += q[i];
+            h[j] = pack8<kT>(p);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int c = tid + j * TPR;
+        gm[j] = c < nchunk ? g[c] : make_uint4(0, 0, 0, 0);
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        float p[8];
+        unpack8<kT>(h[j], p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            ss = __builtin_fmaf(p[i], p[i], ss);
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        ss += __shfl_xor(ss, off, kWave);
+    if constexpr (TPR > kWave) {
+        __shared__ float part[TPR / kWave];
+        if (threadIdx.x % kWave == 0)
+            part[threadIdx.x / kWave] = ss;
+        __syncthreads();
+        ss = 0.0f;
+#pragma unroll
+        for (int w = 0; w < TPR / kWave; ++w)
+            ss += part[w];
+    }
+    if (!live)
+        return;
+    const float rstd = 1.0f / __builtin_sqrtf(ss / (float)a.K + a.eps);
+
+    uint4 *ho = a.H ? reinterpret_cast<uint4 *>(a.H + row * a.K) : nullptr;
+    uint4 *yo = a.Y ? reinterpret_cast<uint4 *>(a.Y + row * a.K) : nullptr;
+    uint2 *qo = reinterpret_cast<uint2 *>(a.Xq + row * a.K);
+    uint8_t *so = a.SX + row * pitch;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int c = tid + j * TPR;
+        const bool in = c < nchunk;
+        float y[8], gg[8];
+        unpack8<kT>(h[j], y);
+        unpack8<kT>(gm[j], gg);
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            y[i] = (y[i] * rstd) * gg[i];
+            m = umax(m, __builtin_bit_cast(unsigned, y[i]) & 0x7fffffffu);
+        }
+        m = group_max<16>(in ? m : 0);
+        const B128Scale sc = b128_scale(m);
+        if (in) {
+            if (ho)
+                ho[c] = h[j];
+            if (yo)
+                yo[c] = pack8<kT>(y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[i] *= sc.mul;
+            qo[c] = cvt8_e4m3(y);
+            if (c % 16 == 0)
+                so[c / 16] = (uint8_t)sc.byte;
+        }
+    }
+    const int nblk = (nchunk + 15) / 16;
+    if (nblk + tid < pitch)
+        so[nblk + tid] = kB128Pad;
+}
+
+template <int TPR, int NC>
+hipError_t launch_norm(const RmsNormArgs &a, int type, hipStream_t s)
+{
+    constexpr int kRows = TPR < kThreads ? kThreads / TPR : 1;
+    const dim3 block(TPR < kThreads ? kThreads : TPR);
+    const int pitch = (int)b128_pitch(a.K);
+    // a launch has fewer than 2^32 threads: more rows go in further launches
+    constexpr int64_t kMost = (int64_t)1 << 21;
+    for (int64_t t0 = 0; t0 < a.T; t0 += kMost) {
+        RmsNormArgs p = a;
+        p.T = a.T - t0 < kMost ? a.T - t0 : kMost;
+        p.X += t0 * a.K;
+        p.R += a.R ? t0 * a.K : 0;
+        p.H += a.H ? t0 * a.K : 0;
+        p.Y += a.Y ? t0 * a.K : 0;
+        p.Xq += t0 * a.K;
+        p.SX += t0 * pitch;
+        const dim3 grid((unsigned)((p.T + kRows - 1) / kRows));
+        if (type == kTypeBf16)
+            hipLaunchKernelGGL((k_rmsnorm_b128<kTypeBf16, TPR, NC>), grid, block, 0, s, p, pitch);
+        else
+            hipLaunchKernelGGL((k_rmsnorm_b128<kTypeF16, TPR, NC>), grid, block, 0, s, p, pitch);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+// ---------------------------------------------------------------------------
+// Activations: a thread takes 16 elements, 8 consecutive lanes a block of 128.
+// Slot i of the launch is slot i % (8 * blocks) of row i / (8 * blocks); the
+// second half of a row's last block has no elements when K ends in half a
+// block.
+// ---------------------------------------------------------------------------
+template <int kT>
+__global__ __launch_bounds__(kThreads) void k_quantize_act_b128(const uint16_t *__restrict__ X,
+                                                                unsigned nslots, unsigned nblk,
+                                                                int64_t K, int pitch,
+                                                                uint8_t *__restrict__ Xq,
+                                                                uint8_t *__restrict__ SX)
+{
+    const unsigned i = blockIdx.x * kThreads + threadIdx.x;
+    const unsigned b = i / 8;
+    const unsigned t = b / nblk, kb = b % nblk;
+    const int64_t k = (int64_t)kb * kB128 + (i % 8) * 16;
+    const bool in = i < nslots && k < K;
+    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+    if (in) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(X + t * K + k);
+        v0 = p[0];
+        v1 = p[1];
+    }
+    const unsigned m = group_max<8>(umax(absmax8(v0), absmax8(v1)));
+    const B128Scale sc = b128_scale(mag_bits_f32<kT>(m));
+    if (in) {
+        const uint2 q0 = quant8_b128<kT>(v0, sc.mul), q1 = quant8_b128<kT>(v1, sc.mul);
+        *reinterpret_cast<uint4 *>(Xq + t * K + k) = make_uint4(q0.x, q0.y, q1.x, q1.y);
+        if (i % 8 == 0) {
+            uint8_t *s = SX + (int64_t)t * pitch + kb;
+            *s = (uint8_t)sc.byte;
+            if (kb + 1 == nblk)
+                for (int p = (int)nblk; p < pitch; ++p)
+                    *++s = kB128Pad;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Weights: a block of 256 threads holds one 128 x 128 block in registers (8
+// chunks of 8 elements per thread, 16 lanes per 256-byte row piece).
+// ---------------------------------------------------------------------------
+template <int kT>
+__global__ __launch_bounds__(kThreads) void k_quantize_weight_b128(
+    const uint16_t *__restrict__ W, int64_t N, int64_t K, int nb, int kbs, int pitch,
+    uint8_t *__restrict__ CB, uint8_t *__restrict__ SB)
+{
+    const int kb = blockIdx.x % kbs;
+    const int64_t r = blockIdx.x / kbs;   // expert * nb + row block
+    const int64_t e = r / nb, n0 = (r % nb) * kB128;
+    const int c = threadIdx.x % 16, r0 = threadIdx.x / 16;
+    const int64_t k = (int64_t)kb * kB128 + 8 * c;
+    const uint16_t *w = W + (e * N + n0) * K + k;
+    uint4 v[8];
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int n = r0 + 16 * j;
+        v[j] = n0 + n < N && k < K ? *reinterpret_cast<const uint4 *>(w + n * K)
+                                   : make_uint4(0, 0, 0, 0);
+        m = umax(m, absmax8(v[j]));
+    }
+    m = wave_max_u32(m);
+    __shared__ unsigned part[kThreads / kWave];
+    if (threadIdx.x % kWave == 0)
+        part[threadIdx.x / kWave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / kWave; ++i)
+        m = umax(m, part[i]);
+    const B128Scale sc = b128_scale(mag_bits_f32<kT>(m));
+    uint8_t *q = CB + (e * N + n0) * K + k;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int n = r0 + 16 * j;
+        if (n0 + n < N && k < K)
+            *reinterpret_cast<uint2 *>(q + n * K) = quant8_b128<kT>(v[j], sc.mul);
+    }
+    if (threadIdx.x == 0) {
+        uint8_t *s = SB + r * pitch + kb;
+        *s = (uint8_t)sc.byte;
+        if (kb + 1 == kbs)
+            for (int p = kbs; p < pitch; ++p)
+                *++s = kB128Pad;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm_b128(const RmsNormArgs &a, int type, hipStream_t s)
+{
+    const int64_t n = a.K / 8;   // chunks per row
+    if (n <= 256 * 2)
+        return launch_norm<256, 2>(a, type, s);
+    if (n <= 256 * 8)
+        return launch_norm<256, 8>(a, type, s);
+    return launch_norm<1024, 17>(a, type, s);   // 17 * 1024 chunks: every supported K
+}
+
+hipError_t launch_quantize_act_b128(const uint16_t *X, int64_t T, int64_t K, int type,
+                                    uint8_t *Xq, uint8_t *SX, hipStream_t s)
+{
+    const int64_t nblk = (K + kB128 - 1) / kB128;
+    const int pitch = (int)b128_pitch(K);
+    // a launch indexes its slots in 32 bits: more rows go in further launches
+    const int64_t most = ((int64_t)1 << 30) / (8 * nblk);
+    for (int64_t t0 = 0; t0 < T; t0 += most) {
+        const int64_t rows = T - t0 < most ? T - t0 : most;
+        const unsigned slots = (unsigned)(rows * nblk * 8);
+        const dim3 grid((slots + kThreads - 1) / kThreads);
+        if (type == kTypeBf16)
+            hipLaunchKernelGGL(k_quantize_act_b128<kTypeBf16>, grid, dim3(kThreads), 0, s,
+                               X + t0 * K, slots, (unsigned)nblk, K, pitch, Xq + t0 * K,
+                               SX + t0 * pitch);
+        else
+            hipLaunchKernelGGL(k_quantize_act_b128<kTypeF16>, grid, dim3(kThreads), 0, s,
+                               X + t0 * K, slots, (unsigned)nblk, K, pitch, Xq + t0 * K,
+                               SX + t0 * pitch);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_quantize_weight_b128(const uint16_t *W, int64_t E, int64_t N, int64_t K,
+                                       int type, uint8_t *CB, uint8_t *SB, hipStream_t s)
+{
+    const int64_t nb = (N + kB128 - 1) / kB128, kbs = (K + kB128 - 1) / kB128;
+    const dim3 grid((unsigned)(E * nb * kbs));
+    const int pitch = (int)b128_pitch(K);
+    if (type == kTypeBf16)
+        hipLaunchKernelGGL(k_quantize_weight_b128<kTypeBf16>, grid, dim3(kThreads), 0, s, W, N, K,
+                           (int)nb, (int)kbs, pitch, CB, SB);
+    else
+        hipLaunchKernelGGL(k_quantize_weight_b128<kTypeF16>, grid, dim3(kThreads), 0, s, W, N, K,
+                           (int)nb, (int)kbs, pitch, CB, SB);
+    return hipGetLastError();
+}
+
+}  // namespace llmint8

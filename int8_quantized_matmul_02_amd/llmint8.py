@@ -46,6 +46,13 @@ EXPORTS = (
     "llmint8_matmul_e4m3_path",
     "llmint8_mfma_ceiling",
     "llmint8_matmul_noalloc",
+    "llmint8_b128_pitch",
+    "llmint8_rmsnorm_b128",
+    "llmint8_quantize_act_b128",
+    "llmint8_quantize_weight_b128",
+    "llmint8_matmul_b128_workspace_bytes",
+    "llmint8_matmul_b128",
+    "llmint8_matmul_grouped_b128",
 )
 
 
@@ -98,7 +105,19 @@ def _load():
                                                                 P, SZ, I, P, P, P]
     lib.llmint8_mfma_ceiling.argtypes = [P, I64, P, I64, I64, I, I, I, P, P, P, P]
     lib.llmint8_matmul_noalloc.argtypes = [P, I64, I64, I64, P, P, P, F, P, P]
-    for fn in ("llmint8_quantize_weight", "llmint8_quantize_act", "llmint8_matmul",
+    lib.llmint8_b128_pitch.argtypes = [I64]
+    lib.llmint8_b128_pitch.restype = I64
+    lib.llmint8_rmsnorm_b128.argtypes = [P, P, P, I, I64, I64, F, P, P, P, P, P]
+    lib.llmint8_quantize_act_b128.argtypes = [P, I, I64, I64, P, P, P]
+    lib.llmint8_quantize_weight_b128.argtypes = [P, I, I64, I64, I64, P, P, P]
+    lib.llmint8_matmul_b128_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.llmint8_matmul_b128_workspace_bytes.restype = SZ
+    lib.llmint8_matmul_b128.argtypes = [P, P, I64, I64, I64, P, P, P, I, I, P, P, SZ, P]
+    lib.llmint8_matmul_grouped_b128.argtypes = [P, P, I64, I64, I64, P, P, I64, P, P, I64, P, I, I,
+                                                P, P]
+    for fn in ("llmint8_rmsnorm_b128", "llmint8_quantize_act_b128", "llmint8_quantize_weight_b128",
+               "llmint8_matmul_b128", "llmint8_matmul_grouped_b128",
+               "llmint8_quantize_weight", "llmint8_quantize_act", "llmint8_matmul",
                "llmint8_matmul_act", "llmint8_matmul_path", "llmint8_igemm_i32",
                "llmint8_quantize_weight_zp", "llmint8_quantize_act_zp", "llmint8_matmul_zp",
                "llmint8_matmul_zp_path", "llmint8_quantize_weight_f8", "llmint8_quantize_act_f8",
@@ -552,3 +571,194 @@ def llmint8_matmul_e4m3_path(X, CB8, SC8, threshold=6.0, bias=None, out=None, ws
 def llmint8_matmul_e4m3(X, CB8, SC8, threshold=6.0, bias=None, out=None, ws=None):
     """The E4M3 decomposition (automatic kernel choice)."""
     return _matmul_fp8("e4m3", X, CB8, SC8, threshold, bias, out, ws)
+
+
+# ---------------------------------------------------------------------------
+# Block-scaled FP8: E4M3 codes with one power-of-two scale (an E8M0 byte) per
+# block of 128.  Codes are uint8 or torch.float8_e4m3fn, scales uint8 or
+# torch.float8_e8m0fnu (the same bytes); what is allocated here is uint8.
+# 16-bit tensors are float16 or bfloat16, all of one call of one dtype.
+# ---------------------------------------------------------------------------
+_TYPES = {torch.float16: 0, torch.bfloat16: 1}
+_T16 = (torch.float16, torch.bfloat16)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def llmint8_b128_pitch(K):
+    """Bytes per row of a scale matrix: ceil(K/128) rounded up to a multiple of 4."""
+    return int(_load().llmint8_b128_pitch(int(K)))
+
+
+def _pitch(K):
+    return (K + 511) // 512 * 4
+
+
+def _tensor(t, name, dtypes, ndim):
+    """An argument that sets a call's sizes: its type, dtype, dimensions and contiguity."""
+    _arg(t, name, dtypes)
+    if t.dim() != ndim:
+        raise ValueError("%s must be %d-D, got shape %s" % (name, ndim, tuple(t.shape)))
+    return t.shape
+
+
+class _on:
+    """The device of a call's tensors made current for its launch, and the
+    stream to use there (a stream handle belongs to its device)."""
+
+    def __init__(self, t):
+        self.dev = t.device
+        self.guard = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.dev.index:
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def llmint8_rmsnorm_b128(X, gamma, eps=1e-6, residual=None, residual_out=None, Y=None, Xq8=None,
+                         SX=None):
+    """RMS norm of X (+ residual) [T,K] with an 8-bit output.  Returns (Xq8 uint8 [T,K],
+    SX uint8 [T,pitch], residual_out [T,K] or None): the codes and scales of the
+    normalized rows and the sum X + residual, which is allocated if there is a residual
+    and none is given (pass `residual` itself to update it in place).  Y: a tensor
+    [T,K] that also receives the normalized rows in X's dtype."""
+    lib = _load()
+    T, K = _tensor(X, "X", _T16, 2)
+    dt = (X.dtype,)
+    d = X.device
+    _arg(gamma, "gamma", dt, shape=(K,))
+    if residual is not None:
+        _arg(residual, "residual", dt, shape=(T, K))
+        residual_out = _new_or(residual_out, "residual_out", dt, (T, K), d)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if Y is not None:
+        _arg(Y, "Y", dt, shape=(T, K))
+    Xq8 = _new_or(Xq8, "Xq8", _CODES, (T, K), d)
+    SX = _new_or(SX, "SX", _SCALES, (T, _pitch(K)), d)
+    _on_device(X=X, gamma=gamma, residual=residual, residual_out=residual_out, Y=Y, Xq8=Xq8, SX=SX)
+    with _on(X) as stream:
+        _check("llmint8_rmsnorm_b128",
+               lib.llmint8_rmsnorm_b128(X.data_ptr(), _ptr(residual), gamma.data_ptr(),
+                                        _TYPES[X.dtype], T, K, float(eps), Xq8.data_ptr(),
+                                        SX.data_ptr(), _ptr(residual_out), _ptr(Y), stream))
+    return Xq8, SX, residual_out
+
+
+def llmint8_quantize_act_b128(X, Xq8=None, SX=None):
+    """X: fp16 or bf16 [T,K].  Returns (Xq8 uint8 [T,K] E4M3 codes, SX uint8 [T,pitch] scales of
+    its 1 x 128 blocks)."""
+    lib = _load()
+    T, K = _tensor(X, "X", _T16, 2)
+    Xq8 = _new_or(Xq8, "Xq8", _CODES, (T, K), X.device)
+    SX = _new_or(SX, "SX", _SCALES, (T, _pitch(K)), X.device)
+    _on_device(X=X, Xq8=Xq8, SX=SX)
+    with _on(X) as stream:
+        _check("llmint8_quantize_act_b128",
+               lib.llmint8_quantize_act_b128(X.data_ptr(), _TYPES[X.dtype], T, K, Xq8.data_ptr(),
+                                             SX.data_ptr(), stream))
+    return Xq8, SX
+
+
+def llmint8_quantize_weight_b128(W_t, CB8=None, SB=None):
+    """W_t: fp16 or bf16 [N,K], or [E,N,K] for the weights of E experts.  Returns (CB8 uint8 of
+    the same shape, SB uint8 [ceil(N/128),pitch] or [E,ceil(N/128),pitch] scales of its
+    128 x 128 blocks)."""
+    lib = _load()
+    _arg(W_t, "W_t", _T16)
+    if W_t.dim() not in (2, 3):
+        raise ValueError("W_t must be [N,K] or [E,N,K], got shape %s" % (tuple(W_t.shape),))
+    N, K = W_t.shape[-2:]
+    E = W_t.shape[0] if W_t.dim() == 3 else 1
+    lead = tuple(W_t.shape[:-2])
+    CB8 = _new_or(CB8, "CB8", _CODES, lead + (N, K), W_t.device)
+    SB = _new_or(SB, "SB", _SCALES, lead + ((N + 127) // 128, _pitch(K)), W_t.device)
+    _on_device(W_t=W_t, CB8=CB8, SB=SB)
+    with _on(W_t) as stream:
+        _check("llmint8_quantize_weight_b128",
+               lib.llmint8_quantize_weight_b128(W_t.data_ptr(), _TYPES[W_t.dtype], E, K, N,
+                                                CB8.data_ptr(), SB.data_ptr(), stream))
+    return CB8, SB
+
+
+def _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, M, lead):
+    """Checks the operands of a product ([E] = lead for the grouped one) and
+    returns its sizes and output; M None: as many rows as Xq8."""
+    T, K = _tensor(Xq8, "Xq8", _CODES, 2)
+    N = _tensor(CB8, "CB8", _CODES, 2 + len(lead))[-2]
+    if CB8.shape[-1] != K:
+        raise ValueError("shape mismatch: Xq8 %s, CB8 %s" % (tuple(Xq8.shape), tuple(CB8.shape)))
+    _arg(SX, "SX", _SCALES, shape=(T, _pitch(K)))
+    _arg(SB, "SB", _SCALES, shape=lead + ((N + 127) // 128, _pitch(K)))
+    if out is not None:
+        _arg(out, "out", _T16, shape=(T if M is None else M, N))
+        out_dtype = out.dtype
+    elif out_dtype not in _TYPES:
+        raise TypeError("out_dtype must be float16 or bfloat16, got %s" % (out_dtype,))
+    if bias is not None:
+        _arg(bias, "bias", (out_dtype,), shape=lead + (N,))
+    if out is None:
+        out = torch.empty((T if M is None else M, N), dtype=out_dtype, device=Xq8.device)
+    return T, K, N, out
+
+
+def llmint8_matmul_b128_workspace_bytes(T, K, N):
+    return int(_load().llmint8_matmul_b128_workspace_bytes(T, K, N))
+
+
+def llmint8_matmul_b128(Xq8, SX, CB8, SB, bias=None, activation=ACT_NONE, out=None,
+                        out_dtype=torch.float16, ws=None):
+    """The product of block-scaled operands: codes Xq8 [T,K] and scales SX (from
+    llmint8_quantize_act_b128 or llmint8_rmsnorm_b128), CB8 [N,K] and SB (from
+    llmint8_quantize_weight_b128) -> out [T,N] in out_dtype (out's own dtype if given;
+    bias [N] has the same)."""
+    lib = _load()
+    T, K, N, out = _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, None, ())
+    need = lib.llmint8_matmul_b128_workspace_bytes(T, K, N)
+    if need or ws is not None:
+        ws = _ws(ws, need, Xq8.device)
+    _on_device(Xq8=Xq8, SX=SX, CB8=CB8, SB=SB, bias=bias, out=out, ws=ws)
+    with _on(Xq8) as stream:
+        _check("llmint8_matmul_b128",
+               lib.llmint8_matmul_b128(Xq8.data_ptr(), SX.data_ptr(), T, K, N, CB8.data_ptr(),
+                                       SB.data_ptr(), _ptr(bias), int(activation),
+                                       _TYPES[out.dtype], out.data_ptr(), _ptr(ws),
+                                       0 if ws is None else _nbytes(ws), stream))
+    return out
+
+
+def llmint8_matmul_grouped_b128(Xq8, SX, CB8, SB, offsets, row_idx=None, bias=None,
+                                activation=ACT_NONE, out=None, out_dtype=torch.float16):
+    """The products of E experts: output rows [offsets[e], offsets[e+1]) use the weight CB8[e]
+    ([E,N,K], scales SB [E,ceil(N/128),pitch], bias [E,N] or None).  offsets int32 [E+1] on the
+    device; row_idx int32 [M] on the device: output row i reads row row_idx[i] of Xq8 (row i
+    without it).  Returns out [M,N]; rows outside [offsets[0], offsets[E]) are left as they were.
+    M = 0 returns the empty output."""
+    lib = _load()
+    if not isinstance(CB8, torch.Tensor) or CB8.dim() != 3:
+        raise ValueError("CB8 must be a tensor [E,N,K]")
+    E = CB8.shape[0]
+    M = None
+    if row_idx is not None:
+        (M,) = _tensor(row_idx, "row_idx", (torch.int32,), 1)
+    T, K, N, out = _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, M, (E,))
+    M = T if M is None else M
+    _arg(offsets, "offsets", (torch.int32,), shape=(E + 1,))
+    _on_device(Xq8=Xq8, SX=SX, CB8=CB8, SB=SB, offsets=offsets, row_idx=row_idx, bias=bias,
+               out=out)
+    if M == 0:
+        return out
+    with _on(Xq8) as stream:
+        _check("llmint8_matmul_grouped_b128",
+               lib.llmint8_matmul_grouped_b128(Xq8.data_ptr(), SX.data_ptr(), T, K, N,
+                                               CB8.data_ptr(), SB.data_ptr(), E,
+                                               offsets.data_ptr(), _ptr(row_idx), M, _ptr(bias),
+                                               int(activation), _TYPES[out.dtype],
+                                               out.data_ptr(), stream))
+    return out

@@ -1,0 +1,169 @@
+"""Block-scaled FP8 operators, what is decided on the CPU: the C entry points'
+argument checks (nothing is enqueued), the binding's, and the float64
+reference that the GPU tests use.  No GPU is needed."""
+import numpy as np
+import pytest
+import torch
+
+from int8_quantized_matmul_02_amd import llmint8 as L
+from tests import b128_ref as ref
+
+P = 0x7F0000000000   # a fake, aligned device address: every call here is rejected before it is used
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    import os
+    if not os.path.exists(L.library_path()):
+        from int8_quantized_matmul_02_amd import build
+        build.build()
+    return L._load()
+
+
+def test_pitch(lib):
+    for K, p in ((64, 4), (128, 4), (512, 4), (576, 8), (4096, 32), (4160, 36), (0, 0), (-64, 0)):
+        assert L.llmint8_b128_pitch(K) == p
+        if K > 0:
+            assert ref.pitch(K) == p == L._pitch(K)
+
+
+def test_norm_refusals(lib):
+    def f(X=P, R=None, G=P, ty=0, T=4, K=128, eps=1e-6, Q=P + BIG, S=P + 2 * BIG, H=None, Y=None):
+        return lib.llmint8_rmsnorm_b128(X, R, G, ty, T, K, eps, Q, S, H, Y, None)
+    for kw in (dict(X=None), dict(G=None), dict(Q=None), dict(S=None), dict(X=P + 8),
+               dict(G=P + 2), dict(R=P + 8), dict(Q=P + 4), dict(S=P + 2), dict(Y=P + 8),
+               dict(H=P + BIG), dict(R=P, H=P + 8), dict(ty=2), dict(ty=-1),
+               dict(eps=float("nan")), dict(eps=-1e-6), dict(eps=float("inf")), dict(T=0),
+               dict(T=-1), dict(K=0)):
+        assert f(**kw) == 1, kw
+    for kw in (dict(K=96), dict(K=133184), dict(T=1 << 31)):
+        assert f(**kw) == 2, kw
+    # in place is allowed, a shifted overlap of the rows is not: 4 rows of 128 are 1024 bytes
+    R = P + (1 << 20)
+    for kw in (dict(R=R, H=R + 16), dict(R=R, H=P + 1008), dict(Y=P + 512), dict(R=R, Y=R - 16),
+               dict(R=R, H=R, Y=R), dict(R=R, H=R + 4096, Y=R + 4096 + 32)):
+        assert f(**kw) == 1, kw
+
+
+def test_quantizer_refusals(lib):
+    def a(X=P, ty=0, T=4, K=128, Q=P, S=P):
+        return lib.llmint8_quantize_act_b128(X, ty, T, K, Q, S, None)
+
+    def w(W=P, ty=0, E=1, K=128, N=128, C=P, S=P):
+        return lib.llmint8_quantize_weight_b128(W, ty, E, K, N, C, S, None)
+    for kw in (dict(X=None), dict(Q=None), dict(S=None), dict(X=P + 8), dict(Q=P + 8),
+               dict(S=P + 1), dict(ty=2), dict(T=0), dict(K=-64)):
+        assert a(**kw) == 1, kw
+    for kw in (dict(W=None), dict(C=None), dict(S=None), dict(W=P + 8), dict(C=P + 8),
+               dict(S=P + 2), dict(ty=3), dict(E=0), dict(N=0), dict(K=0)):
+        assert w(**kw) == 1, kw
+    assert a(K=72) == 2 and a(K=133184) == 2
+    for kw in (dict(K=96), dict(N=96), dict(K=133184), dict(N=(1 << 24) + 64), dict(E=1025)):
+        assert w(**kw) == 2, kw
+
+
+def test_product_refusals(lib):
+    def f(X=P, SX=P, T=4, K=128, N=128, C=P, SB=P, bias=None, act=0, ty=0, out=P, ws=None, wsb=0):
+        return lib.llmint8_matmul_b128(X, SX, T, K, N, C, SB, bias, act, ty, out, ws, wsb, None)
+    for kw in (dict(X=None), dict(SX=None), dict(C=None), dict(SB=None), dict(out=None),
+               dict(X=P + 8), dict(SX=P + 2), dict(C=P + 8), dict(SB=P + 1), dict(bias=P + 4),
+               dict(out=P + 8), dict(ws=P + 8), dict(act=2), dict(act=-1), dict(ty=2), dict(T=0),
+               dict(N=-64)):
+        assert f(**kw) == 1, kw
+    for kw in (dict(K=96), dict(N=96), dict(K=133184), dict(T=1 << 24, N=1 << 24)):
+        assert f(**kw) == 2, kw
+    # argument errors before shape errors
+    assert f(X=None, K=96) == 1
+    assert L.llmint8_matmul_b128_workspace_bytes(0, 128, 128) == 0
+    assert L.llmint8_matmul_b128_workspace_bytes(4, 100, 128) == 0
+
+
+def test_grouped_refusals(lib):
+    def f(X=P, SX=P, T=4, K=128, N=128, C=P, SB=P, E=2, off=P, idx=None, M=4, bias=None, act=0,
+          ty=0, out=P):
+        return lib.llmint8_matmul_grouped_b128(X, SX, T, K, N, C, SB, E, off, idx, M, bias, act,
+                                               ty, out, None)
+    for kw in (dict(X=None), dict(off=None), dict(out=None), dict(off=P + 2), dict(idx=P + 1),
+               dict(bias=P + 4), dict(M=0), dict(M=5), dict(E=0), dict(act=5), dict(ty=9),
+               dict(T=0, M=0)):
+        assert f(**kw) == 1, kw
+    for kw in (dict(E=1025), dict(K=96), dict(N=32), dict(idx=P, M=1 << 31),
+               dict(idx=P, T=1 << 25, K=128), dict(idx=P, M=1 << 30, N=1 << 10)):
+        assert f(**kw) == 2, kw
+
+
+def u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+def test_binding_checks():
+    h, X, s = torch.float16, u8(4, 192), u8(4, 4)
+    C, sb = u8(128, 192), u8(1, 4)
+    Xh, g = torch.zeros((4, 192), dtype=h), torch.zeros(192, dtype=h)
+    bad = [
+        (TypeError, lambda: L.llmint8_rmsnorm_b128(Xh.float(), g)),
+        (TypeError, lambda: L.llmint8_rmsnorm_b128(Xh, g.bfloat16())),
+        (ValueError, lambda: L.llmint8_rmsnorm_b128(Xh, g[:64])),
+        (ValueError, lambda: L.llmint8_rmsnorm_b128(Xh[0], g)),
+        (ValueError, lambda: L.llmint8_rmsnorm_b128(Xh, g, residual_out=Xh)),
+        (ValueError, lambda: L.llmint8_rmsnorm_b128(Xh, g, residual=Xh[:2])),
+        (ValueError, lambda: L.llmint8_rmsnorm_b128(Xh.t().contiguous().t(), g)),
+        (ValueError, lambda: L.llmint8_quantize_act_b128(Xh, Xq8=u8(4, 128))),
+        (ValueError, lambda: L.llmint8_quantize_act_b128(Xh, SX=u8(4, 2))),
+        (ValueError, lambda: L.llmint8_quantize_weight_b128(g)),
+        (ValueError, lambda: L.llmint8_quantize_weight_b128(Xh, SB=u8(4, 4))),
+        (ValueError, lambda: L.llmint8_matmul_b128(X, s, u8(128, 128), sb)),
+        (ValueError, lambda: L.llmint8_matmul_b128(X, u8(4, 2), C, sb)),
+        (ValueError, lambda: L.llmint8_matmul_b128(X, s, C, u8(2, 4))),
+        (TypeError, lambda: L.llmint8_matmul_b128(X.to(torch.int8), s, C, sb)),
+        (TypeError, lambda: L.llmint8_matmul_b128(X, s, C, sb, out_dtype=torch.float32)),
+        (TypeError, lambda: L.llmint8_matmul_b128(X, s, C, sb, bias=torch.zeros(128))),
+        (TypeError, lambda: L.llmint8_matmul_b128(X, s, C, sb, bias=torch.zeros(128, dtype=h),
+                                                  out_dtype=torch.bfloat16)),
+        (ValueError, lambda: L.llmint8_matmul_b128(X, s, C, sb, out=torch.zeros((3, 128), dtype=h))),
+        (ValueError, lambda: L.llmint8_matmul_grouped_b128(X, s, C, sb, u8(2))),
+        (TypeError, lambda: L.llmint8_matmul_grouped_b128(
+            X, s, C[None], sb[None], torch.zeros(2, dtype=torch.int64))),
+        (ValueError, lambda: L.llmint8_matmul_grouped_b128(
+            X, s, C[None], sb[None], torch.zeros(3, dtype=torch.int32))),
+        (TypeError, lambda: L.llmint8_matmul_grouped_b128(
+            X, s, C[None], sb[None], torch.zeros(2, dtype=torch.int32),
+            row_idx=torch.zeros(4, dtype=torch.int64))),
+        (ValueError, lambda: L.llmint8_matmul_grouped_b128(
+            X, s, C[None], sb[None], torch.zeros(2, dtype=torch.int32),
+            bias=torch.zeros(128, dtype=h))),
+    ]
+    for exc, call in bad:
+        with pytest.raises(exc):
+            call()
+    # right in everything but the device
+    for call in (lambda: L.llmint8_rmsnorm_b128(Xh, g), lambda: L.llmint8_quantize_act_b128(Xh),
+                 lambda: L.llmint8_quantize_weight_b128(Xh),
+                 lambda: L.llmint8_matmul_b128(X, s, C, sb),
+                 lambda: L.llmint8_matmul_grouped_b128(X, s, C[None], sb[None],
+                                                       torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="device"):
+            call()
+
+
+def test_reference_codec_against_torch():
+    """The reference's rounding against torch's E4M3 over every binary16 value it covers."""
+    v = torch.arange(0, 0x7c00, dtype=torch.int16).view(torch.float16).float()
+    v = v[v <= 448]
+    got = ref.encode(v.double().numpy())
+    assert np.array_equal(got, v.to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+    codes = np.arange(256, dtype=np.uint8)
+    want = torch.from_numpy(codes).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(ref.decode(codes), want, equal_nan=True)
+
+
+def test_reference_scales():
+    for a, e in ((0.0, 0), (448.0, 0), (448.5, -1), (1.0, 8), (1.75, 8), (1.7500001, 7),
+                 (2.0 ** -133, 126), (2.0 ** -118, 126), (2.0 ** -117, 125), (3.3e38, -120)):
+        assert ref.exponent(a) == e, a
+    v = np.zeros((3, 192))
+    v[1, 5], v[2, 130] = np.inf, -3.5
+    c, s = ref.quantize(v, 1)
+    assert s.tolist() == [[127, 127, 127, 127], [255, 127, 127, 127], [127, 120, 127, 127]]
+    assert np.isnan(ref.values(c, s, 1)[1, :128]).all() and ref.values(c, s, 1)[2, 130] == -3.5

@@ -1,0 +1,469 @@
+"""Block-scaled FP8 operators on the GPU against the float64 reference of
+tests/b128_ref.py: codes and scales of the quantizers bit for bit, the norm's
+within its fp32 error, the products within the bound derived there (and bit
+for bit where every partial sum is exact), ragged groups, infinities and NaN,
+in-place use, streams, graph replay, and the operators in a row."""
+import numpy as np
+import pytest
+import torch
+
+import int8_quantized_matmul_02_amd as L
+from tests import b128_ref as ref
+from tests.gpu_helpers import assert_equal_exact, dev, say
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.float16, torch.bfloat16]
+
+
+def rand(shape, dtype, seed, scale=1.0):
+    return (scale * torch.randn(shape, generator=torch.Generator().manual_seed(seed))).to(dtype)
+
+
+def hidden(T, K, dtype, seed):
+    """Hidden states: N(0,1), a few columns of large magnitude."""
+    x = torch.randn((T, K), generator=torch.Generator().manual_seed(seed))
+    x[:, :: max(1, K // 5)] *= 30.0
+    return x.to(dtype)
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return t.cpu().numpy()
+
+
+def assert_codes(got, want, what):
+    """Bit for bit; any NaN code stands for a NaN."""
+    nan = (want & 127) == 127
+    assert np.array_equal((got & 127) == 127, nan), what + ": NaN codes differ"
+    assert_equal_exact(got[~nan], want[~nan], what)
+
+
+def special_rows(K, dtype):
+    """Rows whose blocks are zero, subnormal, at the format's ends, next to
+    the scale's border 1.75 * 2^E, infinite or NaN."""
+    big, tiny = torch.finfo(dtype).max, torch.finfo(dtype).smallest_normal
+    step = torch.finfo(dtype).eps
+    rows = []
+    for v in (0.0, tiny, -tiny / 4, big, -big, 1.75, 1.75 + step, 1.75 - step, 448.0, 449.0, -0.0,
+              float("inf"), float("-inf"), float("nan")):
+        r = torch.zeros(K)
+        r[3], r[K - 1] = v, v / 3
+        rows.append(r)
+    mixed = torch.linspace(-1, 1, K) * 7
+    mixed[5] = float("nan")
+    return torch.stack(rows + [mixed]).to(dtype)
+
+
+# ---------------------------------------------------------------------------
+# quantizers
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,K", [(1, 64), (1, 128), (3, 192), (17, 576), (257, 1088), (16, 16448),
+                                 (2, 133120)])
+def test_quantize_act(T, K, dtype):
+    say("quantize act", T, K, dtype)
+    X = torch.cat([hidden(T, K, dtype, T + K), special_rows(K, dtype)])
+    q, s = L.llmint8_quantize_act_b128(X.to(dev()))
+    wq, ws = ref.quantize(ref.to64(X), 1)
+    assert_equal_exact(host(s), ws, "scales")
+    assert_codes(host(q), wq, "codes")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E,N,K", [(1, 64, 64), (1, 128, 128), (1, 192, 576), (3, 192, 192),
+                                   (2, 64, 1088), (1, 320, 4160)])
+def test_quantize_weight(E, N, K, dtype):
+    say("quantize weight", E, N, K, dtype)
+    W = rand((E, N, K), dtype, E + N + K, 0.02)
+    W[0, 0, 0] = 1.75
+    W[E - 1, N - 1, K - 1] = float("inf")     # the last block, whole or half
+    if K > 128:
+        W[0, :128, 128:256] = 0
+    q, s = L.llmint8_quantize_weight_b128(W.to(dev()) if E > 1 else W[0].to(dev()))
+    q, s = host(q).reshape(E, N, K), host(s).reshape(E, -1, ref.pitch(K))
+    for e in range(E):
+        wq, ws = ref.quantize(ref.to64(W[e]), 128)
+        assert_equal_exact(s[e], ws, "scales of %d" % e)
+        assert_codes(q[e], wq, "codes of %d" % e)
+
+
+def test_quantizers_take_float8_views():
+    d = dev()
+    X = hidden(5, 320, torch.float16, 1).to(d)
+    q, s = L.llmint8_quantize_act_b128(X)
+    q8 = torch.zeros((5, 320), dtype=torch.float8_e4m3fn, device=d)
+    s8 = torch.zeros((5, 4), dtype=torch.uint8, device=d).view(torch.float8_e8m0fnu)
+    r = L.llmint8_quantize_act_b128(X, Xq8=q8, SX=s8)
+    assert r[0] is q8 and r[1] is s8
+    assert torch.equal(q8.view(torch.uint8), q) and torch.equal(s8.view(torch.uint8), s)
+    W = rand((192, 320), torch.float16, 2, 0.02).to(d)
+    C, S = L.llmint8_quantize_weight_b128(W)
+    a = L.llmint8_matmul_b128(q, s, C, S)
+    b = L.llmint8_matmul_b128(q8, s8, C.view(torch.float8_e4m3fn), S.view(torch.float8_e8m0fnu))
+    assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# norm
+# ---------------------------------------------------------------------------
+# fp32 error of y relative to y: a thread adds at most 136 squares one after
+# another, then 22 partial sums (all positive: relative errors add), halved by
+# the square root; the mean, + eps, root, reciprocal and two products round
+# once each.
+NORM_REL = ((136 + 22) / 2 + 6) * 2.0 ** -24
+
+
+def check_norm(q, s, y, what):
+    """Codes and scales of y (float64): each is the rounding of some value
+    within NORM_REL of y."""
+    T, K = y.shape
+    a = np.abs(ref._blocks(y, 1)).max((2, 3))
+    kb = a.shape[1]
+    lo, hi = ref.exponent(a * (1 + NORM_REL)), ref.exponent(a * (1 - NORM_REL))
+    e = 127 - s[:, :kb].astype(int)
+    assert ((lo <= e) & (e <= hi)).all(), what + ": scales"
+    assert (s[:, kb:] == 127).all(), what + ": padding"
+    m = np.abs(y) * (2.0 ** e).repeat(128, 1)[:, :K]
+    v = np.abs(ref.decode(q))
+    low = ref._E4M3[ref.encode(np.minimum(m * (1 - NORM_REL), 448))]
+    high = ref._E4M3[ref.encode(np.minimum(m * (1 + NORM_REL), 448))]
+    assert ((low <= v) & (v <= high)).all(), what + ": codes"
+    assert (np.signbit(ref.decode(q)) == np.signbit(y))[y != 0].all(), what + ": signs"
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("residual,Y", [(True, True), (False, False), (True, False), (False, True)])
+@pytest.mark.parametrize("T,K", [(1, 64), (5, 128), (257, 192), (3, 576), (33, 1088), (2, 4096),
+                                 (9, 4160), (2, 8256), (1, 16384), (2, 16448), (1, 65600),
+                                 (2, 133120)])
+def test_norm(T, K, residual, Y, dtype):
+    say("norm", T, K, residual, Y, dtype)
+    d = dev()
+    X, g = hidden(T, K, dtype, T + K), (1 + 0.1 * rand((K,), torch.float32, 3)).to(dtype)
+    X[T - 1] = 0 if T > 1 else X[0]          # a zero row: the root of eps alone
+    R = rand((T, K), dtype, 4, 2.0) if residual else None
+    if residual and T > 1:
+        R[T - 1] = 0
+    y = torch.full((T + 1, K), 7.0, dtype=dtype, device=d) if Y else None
+    q, s, h = L.llmint8_rmsnorm_b128(X.to(d), g.to(d), 1e-5, residual=None if R is None else R.to(d),
+                                     Y=y[:T] if Y else None)
+    hw = X + R if residual else X            # one rounding to the type, as the operator's
+    if residual:
+        assert torch.equal(h.cpu(), hw), "residual_out"
+    else:
+        assert h is None
+    h64 = ref.to64(hw)
+    want = h64 / np.sqrt((h64 ** 2).mean(-1, keepdims=True) + np.float64(np.float32(1e-5)))
+    want = want * ref.to64(g)
+    check_norm(host(q), host(s), want, "norm")
+    if Y:
+        got = ref.to64(y)
+        tol = (ref.EPS[dtype] + 2 * NORM_REL) * np.abs(want) + ref.TINY[dtype]
+        assert (np.abs(got[:T] - want) <= tol).all(), "Y"
+        assert (got[T] == 7.0).all(), "the row behind Y"
+
+
+@pytest.mark.parametrize("T,K", [(5, 192), (7, 4096), (3, 20480)])
+def test_norm_in_place(T, K):
+    d, dt = dev(), torch.bfloat16
+    X, R = hidden(T, K, dt, 1).to(d), rand((T, K), dt, 2).to(d)
+    g = torch.ones(K, dtype=dt, device=d)
+    y = torch.empty_like(X)
+    q, s, h = L.llmint8_rmsnorm_b128(X, g, residual=R, Y=y)
+    for into in ("residual", "x"):
+        x2, r2 = X.clone(), R.clone()
+        y2 = x2 if into == "residual" else r2      # y over the other input
+        q2, s2, h2 = L.llmint8_rmsnorm_b128(x2, g, residual=r2, Y=y2,
+                                            residual_out=r2 if into == "residual" else x2)
+        assert torch.equal(h2, h) and torch.equal(y2, y)
+        assert torch.equal(q2, q) and torch.equal(s2, s)
+
+
+def test_norm_infinite_and_nan_rows():
+    """As the formula in fp32: an infinity divides its row to zero but for
+    itself (infinity * 0), a NaN spoils its whole row."""
+    d = dev()
+    X = hidden(3, 384, torch.float16, 5)
+    X[0, 130], X[1, 7] = float("inf"), float("nan")
+    q, s, _ = L.llmint8_rmsnorm_b128(X.to(d), torch.ones(384, dtype=torch.float16, device=d))
+    v = ref.values(host(q), host(s), 1)
+    assert np.isnan(v[0, 128:256]).all() and (v[0, :128] == 0).all() and (v[0, 256:] == 0).all()
+    assert np.isnan(v[1]).all() and np.isfinite(v[2]).all()
+
+
+# ---------------------------------------------------------------------------
+# products
+# ---------------------------------------------------------------------------
+def operands(T, K, N, seed, E=None, exact=False):
+    """(codes and scales of the activations and the weight, on the CPU).
+    exact: few-bit values, scales within a factor of 16, so that every partial
+    sum is a multiple of 2^-8 below 2^15 (K <= 4224) and nothing is rounded."""
+    g = np.random.default_rng(seed)
+    lead = () if E is None else (E,)
+    nb, p = -(-N // 128), ref.pitch(K)
+    if exact:
+        small = np.array([0, 0x30, 0x38, 0x3c, 0x40, 0xb0, 0xb8, 0xbc, 0xc0], np.uint8)
+        return (g.choice(small, (T, K)), g.integers(125, 128, (T, p)).astype(np.uint8),
+                g.choice(small, lead + (N, K)),
+                g.integers(125, 128, lead + (nb, p)).astype(np.uint8))
+    x = g.standard_normal((T, K))
+    x[:, :: max(1, K // 5)] *= 30.0
+    w = 0.02 * g.standard_normal(lead + (N, K))
+    xq, sx = ref.quantize(x, 1)
+    if E is None:
+        return (xq, sx) + ref.quantize(w, 128)
+    qs = [ref.quantize(w[e], 128) for e in range(E)]
+    return xq, sx, np.stack([q for q, _ in qs]), np.stack([s for _, s in qs])
+
+
+def up(*arrays):
+    return [torch.from_numpy(np.ascontiguousarray(a)).to(dev()) for a in arrays]
+
+
+def expect(x, w, bias, relu):
+    """(float64 product, sum of magnitudes)."""
+    v, S = x @ w.T, np.abs(x) @ np.abs(w).T
+    if bias is not None:
+        v, S = v + bias, S + np.abs(bias)
+    return (np.where(v < 0, 0.0, v) if relu else v), S
+
+
+def check_product(got, v, S, K, dtype, exact, what):
+    g = ref.to64(got)
+    if exact:
+        w = torch.from_numpy(v).to(dtype).double().numpy()
+        assert_equal_exact(g, w, what)
+    else:
+        err, tol = np.abs(g - v), ref.product_bound(K, S, v, dtype, wave_sums=16)
+        assert not np.isnan(g).any(), what
+        assert (err <= tol).all(), "%s: worst %.3g of its bound" % (what, (err / tol).max())
+
+
+ROWS = [1, 2, 7, 15, 16, 17, 31, 33, 64, 65, 100, 129, 256, 257, 300]
+
+
+@pytest.mark.parametrize("exact", [True, False])
+@pytest.mark.parametrize("K,N", [(64, 64), (128, 128), (192, 192), (320, 64), (512, 320),
+                                 (576, 1088), (1024, 256), (1088, 576), (4160, 192)])
+def test_matmul(K, N, exact):
+    for i, T in enumerate(ROWS):
+        dtype, bias, relu = TYPES[i % 2], (i + K // 64) % 3 != 0, i % 3 == 1
+        say("matmul", T, K, N, dtype, "bias" * bias, "relu" * relu, "exact" * exact)
+        xq, sx, wq, sw = operands(T, K, N, T + K + N, exact=exact)
+        b = rand((N,), dtype, N)
+        b = (b * 4).round() / 4 if exact else b
+        out = torch.full((T + 2, N), 9.0, dtype=dtype, device=dev())
+        L.llmint8_matmul_b128(*up(xq, sx, wq, sw), bias=b.to(dev()) if bias else None,
+                              activation=L.ACT_RELU if relu else L.ACT_NONE, out=out[:T])
+        v, S = expect(ref.values(xq, sx, 1), ref.values(wq, sw, 128),
+                      ref.to64(b) if bias else None, relu)
+        check_product(out[:T], v, S, K, dtype, exact, "T=%d K=%d N=%d" % (T, K, N))
+        assert (out[T:] == 9.0).all(), "rows behind the output"
+
+
+@pytest.mark.parametrize("T", [4, 60, 300])
+def test_matmul_range_of_scales(T):
+    """Scales at both ends: products that overflow to infinity, vanish to
+    zero, and a NaN block that reaches its rows and columns alone."""
+    K, N = 320, 256
+    xq, sx, wq, sw = operands(T, K, N, 3, exact=True)
+    xq[:], wq[:] = 0x38, 0x38                          # all ones
+    sx[:], sw[:] = 127, 127
+    sx[0, 0], sx[1, :3], sx[2, 1] = 127 + 60, 1, 255   # row 0: huge, 1: tiny, 2: NaN
+    sw[1, 2] = 127 + 90
+    a = up(xq, sx, wq, sw)
+    v = ref.values(xq, sx, 1) @ ref.values(wq, sw, 128).T
+    for dtype in TYPES:
+        for act in (L.ACT_NONE, L.ACT_RELU):
+            got = ref.to64(L.llmint8_matmul_b128(*a, out_dtype=dtype, activation=act))
+            want = torch.from_numpy(v).to(dtype).double().numpy()
+            assert np.array_equal(np.isnan(got), np.isnan(want))
+            assert np.array_equal(np.nan_to_num(got, nan=1), np.nan_to_num(want, nan=1))
+
+
+GROUPS = [
+    # rows of each expert
+    [5], [0, 3, 0], [1, 1, 1, 1], [16, 17, 0, 1], [0, 0, 40], [70, 0, 129, 2], [300, 5, 0, 31, 64],
+    [0, 0], [1] * 70 + [0] * 60 + [3], [20] * 33,
+]
+
+
+@pytest.mark.parametrize("exact", [True, False])
+@pytest.mark.parametrize("K,N", [(64, 64), (192, 320), (576, 192), (1088, 128)])
+def test_grouped(K, N, exact):
+    d = dev()
+    for i, rows in enumerate(GROUPS):
+        E, gather, bias, relu = len(rows), i % 2 == 0, i % 3 != 1, i % 4 == 1
+        dtype = TYPES[i // 2 % 2]
+        first = 3 if i % 3 == 0 else 0                   # rows before and behind all groups
+        M = first + sum(rows) + (5 if i % 2 else 0)
+        M = max(M, 1)
+        say("grouped", rows[:8], E, K, N, dtype, "gather" * gather, "exact" * exact)
+        T = 11 if gather else M
+        xq, sx, wq, sw = operands(T, K, N, 100 + i + K, E=E, exact=exact)
+        idx = np.random.default_rng(i).integers(0, T, M).astype(np.int32)
+        off = (first + np.concatenate([[0], np.cumsum(rows)])).astype(np.int32)
+        b = rand((E, N), dtype, N)
+        b = (b * 4).round() / 4 if exact else b
+        out = torch.full((M, N), 9.0, dtype=dtype, device=d)
+        r = L.llmint8_matmul_grouped_b128(*up(xq, sx, wq, sw, off),
+                                          row_idx=up(idx)[0] if gather else None,
+                                          bias=b.to(d) if bias else None, out=out,
+                                          activation=L.ACT_RELU if relu else L.ACT_NONE)
+        assert r is out
+        x = ref.values(xq, sx, 1)
+        x = x[idx] if gather else x
+        for e in range(E):
+            lo, hi = off[e], off[e + 1]
+            v, S = expect(x[lo:hi], ref.values(wq[e], sw[e], 128),
+                          ref.to64(b)[e] if bias else None, relu)
+            check_product(out[lo:hi], v, S, K, dtype, exact, "%s expert %d" % (rows[:8], e))
+        assert (out[:first] == 9.0).all() and (out[off[-1]:] == 9.0).all(), "rows of no group"
+
+
+def test_grouped_without_rows():
+    d = dev()
+    xq, sx, wq, sw = up(*operands(4, 128, 64, 1, E=2))
+    none = torch.zeros(0, dtype=torch.int32, device=d)
+    r = L.llmint8_matmul_grouped_b128(xq, sx, wq, sw, torch.zeros(3, dtype=torch.int32, device=d),
+                                      row_idx=none)
+    assert r.shape == (0, 64)
+
+
+def test_grouped_equals_single_products():
+    """One expert's rows give the bits of the plain product's, and a row does
+    not depend on the others of its group."""
+    d = dev()
+    xq, sx, wq, sw = up(*operands(40, 576, 192, 7, E=3))
+    off = torch.tensor([0, 8, 8, 40], dtype=torch.int32, device=d)
+    out = L.llmint8_matmul_grouped_b128(xq, sx, wq, sw, off)
+    again = L.llmint8_matmul_grouped_b128(xq, sx, wq, sw, off)
+    assert torch.equal(out, again)
+    alone = L.llmint8_matmul_grouped_b128(
+        xq, sx, wq, sw, torch.tensor([0, 0, 0, 1], dtype=torch.int32, device=d),
+        row_idx=torch.tensor([39], dtype=torch.int32, device=d))
+    a, b = ref.to64(alone[0]), ref.to64(out[39])
+    assert (np.abs(a - b) <= 2 * ref.EPS[torch.float16] * np.abs(b) + 1e-3).all()
+
+
+# ---------------------------------------------------------------------------
+# use
+# ---------------------------------------------------------------------------
+def chain(X, R, g, Wr, W1, W2):
+    """A feed-forward block with experts, as a model runs it: norm, a router
+    on its 16-bit output, rows in expert order, both grouped products, and the
+    weighted sum of each token's experts."""
+    T, (C1, S1), (C2, S2) = X.shape[0], W1, W2
+    E, top = C1.shape[0], 2
+    y = torch.empty_like(X)
+    q, s, h = L.llmint8_rmsnorm_b128(X, g, residual=R, Y=y)
+    p, pick = torch.softmax(y.float() @ Wr, -1).topk(top)
+    order = pick.reshape(-1).sort(stable=True)
+    off = torch.searchsorted(order.values, torch.arange(E + 1, device=X.device)).to(torch.int32)
+    tok = (order.indices // top).to(torch.int32)
+    z = L.llmint8_matmul_grouped_b128(q, s, C1, S1, off, row_idx=tok, activation=L.ACT_RELU,
+                                      out_dtype=X.dtype)
+    zq, zs = L.llmint8_quantize_act_b128(z)
+    o = L.llmint8_matmul_grouped_b128(zq, zs, C2, S2, off, out_dtype=X.dtype)
+    w = p.reshape(-1)[order.indices]
+    return (h.float().index_add(0, tok.long(), o.float() * w[:, None])), q, s, off, tok, z, zq, zs, o
+
+
+@pytest.mark.parametrize("T", [1, 19, 300])
+def test_operators_in_a_row(T):
+    say("chain", T)
+    d, dt, K, F, E = dev(), torch.bfloat16, 320, 576, 6
+    X, R = hidden(T, K, dt, T).to(d), rand((T, K), dt, 1).to(d)
+    g = (1 + 0.1 * rand((K,), torch.float32, 2)).to(dt).to(d)
+    Wr = rand((K, E), torch.float32, 3).to(d)
+    W1 = L.llmint8_quantize_weight_b128(rand((E, F, K), dt, 4, 0.05).to(d))
+    W2 = L.llmint8_quantize_weight_b128(rand((E, K, F), dt, 5, 0.05).to(d))
+    y, q, s, off, tok, z, zq, zs, o = chain(X, R, g, Wr, W1, W2)
+    # each step against the reference on what it was given
+    off, tok = host(off), host(tok)
+    x = ref.values(host(q), host(s), 1)[tok]
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        v, S = expect(x[a:b], ref.values(host(W1[0][e]), host(W1[1][e]), 128), None, True)
+        check_product(z[a:b], v, S, K, dt, False, "first product, expert %d" % e)
+    wq, ws = ref.quantize(ref.to64(z), 1)
+    assert_equal_exact(host(zs), ws, "scales between")
+    assert_codes(host(zq), wq, "codes between")
+    x = ref.values(wq, ws, 1)
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        v, S = expect(x[a:b], ref.values(host(W2[0][e]), host(W2[1][e]), 128), None, False)
+        check_product(o[a:b], v, S, F, dt, False, "second product, expert %d" % e)
+    assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_graph_replay(T):
+    """All operators captured in one graph: every replay, between eager work,
+    gives the eager bits, also for new inputs and new group sizes."""
+    say("graph", T)
+    d, dt, K, N, E = dev(), torch.float16, 576, 320, 4
+    X, X2 = hidden(T, K, dt, 1).to(d), hidden(T, K, dt, 2).to(d)
+    R, g = rand((T, K), dt, 3).to(d), torch.ones(K, dtype=dt, device=d)
+    W = rand((E, N, K), dt, 4, 0.05).to(d)
+    C, S = L.llmint8_quantize_weight_b128(W)
+    cut = lambda *b: torch.tensor([min(v, T) for v in b], dtype=torch.int32, device=d)  # noqa: E731
+    off, off2 = cut(0, T // 3, T // 3, T // 2, T), cut(0, 0, 1, T, T)
+    ws = torch.empty((max(1, L.llmint8_matmul_b128_workspace_bytes(T, K, N)),), dtype=torch.uint8,
+                     device=d)
+
+    def buffers():
+        return (torch.empty((T, K), dtype=torch.uint8, device=d),
+                torch.empty((T, L.llmint8_b128_pitch(K)), dtype=torch.uint8, device=d),
+                torch.empty((T, K), dtype=dt, device=d), torch.empty((T, N), dtype=dt, device=d),
+                torch.empty((T, N), dtype=dt, device=d))
+
+    def call(x, o, b):
+        q, s, h, v, w = b
+        L.llmint8_rmsnorm_b128(x, g, residual=R, Xq8=q, SX=s, residual_out=h)
+        L.llmint8_matmul_b128(q, s, C[0], S[0], out=v, ws=ws)
+        L.llmint8_quantize_act_b128(h, Xq8=q, SX=s)
+        L.llmint8_matmul_grouped_b128(q, s, C, S, o, out=w)
+
+    want, want2, got = buffers(), buffers(), buffers()
+    call(X, off, want)
+    call(X2, off2, want2)
+    x, o = X.clone(), off.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(x, o, got)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(x, o, got)
+    for rep in range(4):
+        for t in got:
+            t.fill_(3)
+        ws.fill_(0x5a)
+        if rep == 2:
+            x.copy_(X2)
+            o.copy_(off2)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want if rep < 2 else want2):
+            assert torch.equal(a, b), "replay %d" % rep
+
+
+def test_two_streams_at_once():
+    """Calls on two streams at the same time do not disturb each other."""
+    d = dev()
+    data = [up(*operands(T, 1088, 576, T)) for T in (33, 300)]
+    want = [L.llmint8_matmul_b128(*a) for a in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(L.llmint8_matmul_b128(*data[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(g, want[i]) for g in got[i])
