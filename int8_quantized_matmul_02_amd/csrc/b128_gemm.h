@@ -19,10 +19,9 @@
 //
 // Two kernels:
 //  * k_b128_big streams 128-byte stages of both operands through an LDS ring
-//    into v_mfma_scale_f32_32x32x64 (many rows: bound by the matrix cores);
-//  * k_b128_small streams 512-byte stages into v_mfma_scale_f32_16x16x128 and
-//    splits each stage's blocks of K over the wavefronts of a block (few rows:
-//    bound by reading the weight).
+//    (many rows: bound by the matrix cores);
+//  * k_b128_small streams 512-byte stages and splits each stage's blocks of K
+//    over the wavefronts of a block (few rows: bound by reading the weight).
 #pragma once
 
 #include "b128.h"
@@ -58,62 +57,77 @@ __device__ __forceinline__ int group_tiles(const B128Args &a, int base, int lane
     return (hi - lo + bm - 1) / bm;
 }
 
-__device__ __forceinline__ int wave_prefix_sum(int v, int lane)
+// v of lanes 0 .. l summed into lane l, by data-parallel moves: within rows of
+// 16, then rows 0 and 2 into 1 and 3, then the lower half into the upper.
+__device__ __forceinline__ int wave_prefix_sum(int v)
 {
-#pragma unroll
-    for (int off = 1; off < kWave; off *= 2) {
-        const int up = __shfl_up(v, off, kWave);
-        v += lane >= off ? up : 0;
-    }
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);   // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);   // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);   // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31
     return v;
 }
 
-// The tile of block `bid`; false for a block past the last one.  Every
-// wavefront of the block computes it, from the same data.
+// Finds tiles by number.  A plain product's are a grid; a grouped one's are
+// counted per expert, 64 experts at a time (the first 64 stay in registers).
 template <int BM, int BN, int GROUP>
-__device__ __forceinline__ bool find_tile(const B128Args &a, int lane, Tile &t)
-{
-    const int ntn = (int)((a.N + BN - 1) / BN);
-    int tm, tn;
-    if (!a.offsets) {
-        const int ntm = (int)((a.M + BM - 1) / BM);
-        gemm::tile_coords(blockIdx.x, ntm * ntn, ntm, ntn, GROUP, tm, tn);
+struct Tiles {
+    int ntm, ntn;
+    int lo, hi, own, sum;   // this lane's expert of the first 64
+
+    __device__ __forceinline__ void init(const B128Args &a, int lane)
+    {
+        ntn = (int)((a.N + BN - 1) / BN);
+        lo = hi = own = sum = 0;
+        if (!a.offsets) {
+            ntm = (int)((a.M + BM - 1) / BM);
+            return;
+        }
+        own = group_tiles(a, 0, lane, BM, lo, hi);
+        sum = wave_prefix_sum(own);
+        ntm = __builtin_amdgcn_readlane(sum, kWave - 1);
+        for (int base = kWave; base < a.E; base += kWave) {
+            int l, h;
+            ntm += __builtin_amdgcn_readlane(wave_prefix_sum(group_tiles(a, base, lane, BM, l, h)),
+                                             kWave - 1);
+        }
+    }
+    __device__ __forceinline__ int count() const { return ntm * ntn; }
+
+    // Tile v < count(): workgroup ids are dealt round-robin over the XCDs, so
+    // each XCD takes a contiguous run of tiles, which walk GROUP tile rows at
+    // a time.
+    __device__ __forceinline__ Tile find(const B128Args &a, int v, int lane) const
+    {
+        Tile t;
+        int tm, tn;
+        gemm::tile_coords(v, ntm * ntn, ntm, ntn, GROUP, tm, tn);
+        t.n0 = (int64_t)tn * BN;
         t.e = 0;
         t.m0 = tm * BM;
         t.mend = (int)a.M;
-        t.n0 = (int64_t)tn * BN;
-        return true;
-    }
-    int ntm = 0, lo, hi;
-    for (int base = 0; base < a.E; base += kWave) {
-        int n = group_tiles(a, base, lane, BM, lo, hi);
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1)
-            n += __shfl_xor(n, off, kWave);
-        ntm += n;
-    }
-    ntm = __builtin_amdgcn_readfirstlane(ntm);
-    if ((int)blockIdx.x >= ntm * ntn)
-        return false;
-    gemm::tile_coords(blockIdx.x, ntm * ntn, ntm, ntn, GROUP, tm, tn);
-    t.n0 = (int64_t)tn * BN;
-    int before = 0;
-    for (int base = 0; base < a.E; base += kWave) {
-        const int own = group_tiles(a, base, lane, BM, lo, hi);
-        const int sum = wave_prefix_sum(own, lane);
-        const unsigned long long hit = __ballot(before + sum > tm);
-        if (hit) {
-            const int l = __builtin_amdgcn_readfirstlane(__builtin_ctzll(hit));
-            const int first = before + __builtin_amdgcn_readlane(sum - own, l);
-            t.e = base + l;
-            t.m0 = __builtin_amdgcn_readlane(lo, l) + (tm - first) * BM;
-            t.mend = __builtin_amdgcn_readlane(hi, l);
-            return true;
+        if (!a.offsets)
+            return t;
+        int l0 = lo, h0 = hi, o0 = own, s0 = sum, before = 0;
+        for (int base = 0;;) {
+            const unsigned long long hit = __ballot(before + s0 > tm);
+            if (hit) {
+                const int l = __builtin_amdgcn_readfirstlane(__builtin_ctzll(hit));
+                t.e = base + l;
+                t.m0 = __builtin_amdgcn_readlane(l0, l) +
+                       (tm - before - __builtin_amdgcn_readlane(s0 - o0, l)) * BM;
+                t.mend = __builtin_amdgcn_readlane(h0, l);
+                return t;
+            }
+            before += __builtin_amdgcn_readlane(s0, kWave - 1);
+            base += kWave;
+            o0 = group_tiles(a, base, lane, BM, l0, h0);
+            s0 = wave_prefix_sum(o0);
         }
-        before += __builtin_amdgcn_readlane(sum, kWave - 1);
     }
-    return false;
-}
+};
 
 // The activation row of output row i (rows past the group's end: its last).
 __device__ __forceinline__ int64_t source_row(const B128Args &a, const Tile &t, int64_t i)
@@ -132,9 +146,11 @@ __device__ __forceinline__ int64_t scale_rows(const B128Args &a) { return (a.N +
 // through a buffer resource based at `base`, with a fixed 32-bit offset per
 // lane and the stage's byte of K as the scalar offset.  Past the end of the
 // resource a load gives zeros.
+constexpr uint32_t kNowhere = 0xfffffff0u;   // an offset outside every resource
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t *base, int64_t bytes)
 {
-    const uint32_t n = bytes > 0xffffffffll ? 0xffffffffu : (uint32_t)bytes;
+    constexpr int64_t kMost = 0xffe00000;   // soffset, at most K, does not reach kNowhere from here
+    const uint32_t n = (uint32_t)(bytes > kMost ? kMost : bytes);
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), (short)0, (int)n,
                                              0x00020000);
 }
@@ -158,24 +174,25 @@ __device__ __forceinline__ unsigned buf_load4(__amdgpu_buffer_rsrc_t r, uint32_t
     return __builtin_amdgcn_raw_buffer_load_b32(r, voffset, soffset, 0);
 }
 
-// Four finished outputs of consecutive columns: bias, activation, rounding.
-// An activation keeps a NaN.
+// Four finished outputs of consecutive columns: bias (0 without one),
+// activation (lowest: 0, or -infinity without one; a NaN stays), rounding.
+// No branches, so that the callers' unrolled loops stay straight.
 template <int kT>
-__device__ __forceinline__ uint2 finish4(v4f v, bool bias, uint2 b, int act)
+__device__ __forceinline__ uint2 finish4(v4f v, uint2 b, float lowest)
 {
-    if (bias) {
-        v[0] += t2f<kT>((uint16_t)b.x);
-        v[1] += t2f<kT>((uint16_t)(b.x >> 16));
-        v[2] += t2f<kT>((uint16_t)b.y);
-        v[3] += t2f<kT>((uint16_t)(b.y >> 16));
-    }
-    if (act) {
+    v[0] += t2f<kT>((uint16_t)b.x);
+    v[1] += t2f<kT>((uint16_t)(b.x >> 16));
+    v[2] += t2f<kT>((uint16_t)b.y);
+    v[3] += t2f<kT>((uint16_t)(b.y >> 16));
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            v[q] = v[q] < 0.0f ? 0.0f : v[q];
-    }
+    for (int q = 0; q < 4; ++q)
+        v[q] = v[q] < lowest ? lowest : v[q];
     return make_uint2(f2t<kT>(v[0]) | (unsigned)f2t<kT>(v[1]) << 16,
                       f2t<kT>(v[2]) | (unsigned)f2t<kT>(v[3]) << 16);
+}
+__device__ __forceinline__ float lowest_output(const B128Args &a)
+{
+    return a.act ? 0.0f : -__builtin_inff();
 }
 
 // ---------------------------------------------------------------------------
@@ -222,9 +239,11 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
     __shared__ __attribute__((aligned(1024))) char smem[C::kLdsBytes];
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    Tile t;
-    if (!find_tile<C::BM, C::BN, C::GROUP>(a, lane, t))
+    Tiles<C::BM, C::BN, C::GROUP> tiles;
+    tiles.init(a, lane);
+    if ((int)blockIdx.x >= tiles.count())
         return;
+    const Tile t = tiles.find(a, blockIdx.x, lane);
     const int wn = wave % C::WN, wm = wave / C::WN % C::WM, wk = wave / (C::WN * C::WM);
     const int64_t pitch = b128_pitch(a.K);
     const int nblk = (int)((a.K + kB128 - 1) / kB128), nst = (nblk + 3) / 4;
@@ -333,6 +352,7 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
                                      (wk * C::BM + (wm * C::FM + i) * 16 + r) * C::kSumPitch +
                                      (wn * C::FN + j) * 16 + 4 * g) = acc[i][j];
     __syncthreads();
+    const float lowest = lowest_output(a);
     constexpr int kUnits = C::BN / 4;
     for (int u = tid; u < C::BM * kUnits; u += C::kThreads) {
         const int row = u / kUnits, c = u % kUnits * 4;
@@ -349,246 +369,372 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
         if (a.bias)
             b = *reinterpret_cast<const uint2 *>(a.bias + (int64_t)t.e * a.N + n);
         uint2 *o = reinterpret_cast<uint2 *>(a.out + (int64_t)(t.m0 + row) * a.N + n);
-        if (a.type == kTypeBf16)
-            *o = finish4<kTypeBf16>(v, a.bias != nullptr, b, a.act);
-        else
-            *o = finish4<kTypeF16>(v, a.bias != nullptr, b, a.act);
+        *o = a.type == kTypeBf16 ? finish4<kTypeBf16>(v, b, lowest) : finish4<kTypeF16>(v, b, lowest);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Many rows.  BM x BN outputs per block, WM x WN wavefronts of FM x FN tiles
-// of 32 x 32, stages of one block of K (128 bytes of each row) in a ring of
-// two LDS buffers filled by direct global->LDS loads; the swizzle of the
-// staged rows is gemm::Cfg's.  A lane's scales of four blocks (its FM rows'
-// and the weight's) are one dword each, loaded four stages ahead and shifted
-// down by a byte per stage.
+// Many rows.  BM x BN outputs per tile, WM x WN wavefronts of FM x FN tiles of
+// 16 x 16, stages of one block of K (128 bytes of each row) in a ring of
+// STAGES LDS buffers filled by direct global->LDS loads of whole lines.
+//
+// v_mfma_scale_f32_16x16x128 rather than 32x32x64: half the accumulator
+// traffic per product.  Both have the same rate, but the card is held by its
+// power limit here, and registers-only loops over real codes ran 4160 TFLOP/s
+// against 3830.
+//
+// One instruction takes a whole block of K, so a stage is one k-step.  Its
+// MFMAs go by pairs of row tiles, column by column, and the fragments of
+// stage s + 1 are read from LDS into the registers of stage s as these come
+// free: A's tiles after their pair, B's column tiles one after another during
+// the last pair (the last pair's A tiles at the start of the next stage).  By
+// the time the first pair is through, all reads of a stage are long done: the
+// one barrier of a stage sits there, and behind it stage s + STAGES is loaded
+// into the buffer that s has left.
+//
+// Blocks are persistent: a block takes tiles v, v + grid, ..., and loads the
+// next tile's first stages before it writes a finished tile out.  Past a
+// tile's last stage the loads go through an empty resource, which returns
+// zeros without reading memory, so that every stage issues the same loads and
+// the waits are constants.
+//
+// The 16-byte chunk c of staged row r sits in slot c ^ (r / 2 % 8); a lane's
+// 32 bytes of a block are chunks g and g + 4 (g = lane / 16), the same for
+// both operands.  A last block of 64 columns is staged with zeros for chunks
+// 4 .. 7 (their lanes' offsets lie outside the resource).  The scales of 16
+// stages (16 bytes of each row) are loaded into LDS together, a chunk ahead,
+// in two buffers, and read a byte per row tile and stage.  (Loads of scales
+// into registers made the compiler wait for all loads in flight once per
+// stage.)
 // ---------------------------------------------------------------------------
-template <class C>
-struct BigLoads {
-    __amdgpu_buffer_rsrc_t ra, rb;
-    uint32_t offA[C::kAInstr], offB[C::kBInstr];
-
-    __device__ __forceinline__ void init(const B128Args &a, const Tile &t, int wave, int lane)
-    {
-        const int64_t xr = x_base_row(a, t), wr = (int64_t)t.e * a.N + t.n0;
-        ra = resource(a.Xq + xr * a.K, (a.rows - xr) * a.K);
-        rb = resource(a.CB + wr * a.K, ((int64_t)a.E * a.N - wr) * a.K);
-        const int lr = lane / C::kChunks, ls = lane % C::kChunks;
-#pragma unroll
-        for (int j = 0; j < C::kAInstr; ++j) {
-            const int r = (wave * C::kAInstr + j) * C::kRowsPerInstr + lr;
-            const int64_t row = source_row(a, t, t.m0 + r) - xr;
-            offA[j] = (uint32_t)(row * a.K + ((ls ^ C::swz(r)) << 4));
-        }
-#pragma unroll
-        for (int j = 0; j < C::kBInstr; ++j) {
-            const int r = (wave * C::kBInstr + j) * C::kRowsPerInstr + lr;
-            const int64_t row = t.n0 + r < a.N ? r : a.N - 1 - t.n0;   // ragged: clamp
-            offB[j] = (uint32_t)(row * a.K + ((ls ^ C::swz(r)) << 4));
-        }
-    }
-    __device__ __forceinline__ void issue_one(char *smem, int buf, uint32_t kbyte, int wave,
-                                              int j) const
-    {
-        char *sa = smem + buf * C::kStageBytes;
-        char *sb = sa + C::BM * C::ROWB;
-        if (j < C::kAInstr)
-            gemm::lds_load16(ra, (lds_void *)(sa + (wave * C::kAInstr + j) * 1024), offA[j], kbyte);
-        else
-            gemm::lds_load16(rb, (lds_void *)(sb + (wave * C::kBInstr + j - C::kAInstr) * 1024),
-                             offB[j - C::kAInstr], kbyte);
-    }
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int GROUP_>
+struct BigCfg {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_, GROUP = GROUP_;
+    static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+    static constexpr int kTM = BM / WM, kTN = BN / WN;         // a wavefront's rows and columns
+    static constexpr int FM = kTM / 16, FN = kTN / 16;
+    static constexpr int kAInstr = BM / 8 / kWaves, kBInstr = BN / 8 / kWaves;
+    static constexpr int kLoads = kAInstr + kBInstr;           // 1 KB loads per wavefront and stage
+    static constexpr int kStageBytes = (BM + BN) * 128;
+    static constexpr int kRing = STAGES * kStageBytes;
+    static constexpr int kOutBytes = 16 * kTN * 2;             // a wavefront's output staging
+    static constexpr int kChunk = 16;                          // stages per chunk of scales
+    static constexpr int kScaleRows = BM * kChunk;             // then 256 bytes per wavefront: its columns'
+    static constexpr int kScaleBytes = kScaleRows + kWaves * 256;
+    static constexpr int kOut = kRing + 2 * kScaleBytes;
+    static constexpr int kLdsBytes = kOut + kWaves * kOutBytes;
+    static constexpr int kPerCu = 160 * 1024 / kLdsBytes;      // resident blocks per CU
+    static_assert(BM % (8 * kWaves) == 0 && BN % (16 * kWaves) == 0, "load split");
+    static_assert(kTN <= kB128 && kB128 % kTN == 0, "a wavefront's columns share a scale row");
+    static_assert(FM >= 4 && FM % 2 == 0 && kLoads <= (FM - 2) * FN, "issue slots");
+    static_assert(STAGES >= 2 && (STAGES - 1) * kLoads < 64, "vmcnt range");
+    static_assert(kPerCu >= 1, "LDS");
+    static_assert(BM == 64 * kWaves || BM == 32 * kWaves, "scales: a row per lane");
 };
 
 // Keeps the MFMAs on `v` between the side-effecting operations around this
 // point: an MFMA is a pure value to the compiler, which otherwise gathers a
-// k-step's MFMAs in one run and leaves the loads and reads between two runs.
-__device__ __forceinline__ void pin(v16f &v) { asm volatile("" : "+a"(v)); }
+// stage's MFMAs in one run and leaves the loads and reads behind it (273 us
+// against 240 at 4096 x 4096 x 16384, in an earlier form of this kernel).
+__device__ __forceinline__ void pin(v4f &v) { asm volatile("" : "+a"(v)); }
 
-// One 64-deep k-step in a fixed issue order: before each MFMA its share of the
-// fragment reads of the next k-step and of kNL loads of the stage being
-// refilled, so that both run under the MFMAs.
-template <class C, int kNL>
-__device__ __forceinline__ void kstep(const gemm::Frags8<C> &cur, gemm::Frags8<C> &nxt,
-                                      const char *sa, const char *sb, int fo0, int fo1,
-                                      v16f (&acc)[C::FM][C::FN], const unsigned (&sx)[C::FM],
-                                      unsigned sw, const BigLoads<C> &ld, char *smem, int buf,
-                                      uint32_t kbyte, int wave)
+__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+
+// The stage loads of a block, running ahead of its products.  Scalar offsets
+// stay below a resource's size (one row at least), as its range check needs.
+template <class C, bool kGather>
+struct Loader {
+    const uint8_t *pa, *pb;
+    int64_t na, nb;            // bytes of the resources
+    uint32_t off[C::kLoads];   // this lane's offset of each load, A's first
+    uint32_t upper[2];         // by a load's parity: kNowhere if the lane's chunk is one of 4 .. 7
+
+    __device__ __forceinline__ void init(const B128Args &a, const Tile &t, int wave, int lane)
+    {
+        static_assert(C::kAInstr % 2 == 0 && C::kBInstr % 2 == 0, "parity of a row group");
+        const int64_t xr = kGather ? 0 : t.m0, wr = (int64_t)t.e * a.N + t.n0;
+        // rows past the group's end, and columns past N, give zeros or
+        // another expert's weights: outputs that are not stored
+        pa = a.Xq + xr * a.K;
+        na = ((kGather ? a.rows : t.mend) - xr) * a.K;
+        pb = a.CB + wr * a.K;
+        nb = ((int64_t)a.E * a.N - wr) * a.K;
+        const int lr = lane / 8, ls = lane % 8;
+        // row r of the tile: its chunk in slot ls is ls ^ swz(r)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+            upper[p] = (ls ^ swz(p * 8 + lr)) & 4 ? kNowhere : 0;
+#pragma unroll
+        for (int j = 0; j < C::kLoads; ++j) {
+            const bool isa = j < C::kAInstr;
+            const int r = (isa ? wave * C::kAInstr + j : wave * C::kBInstr + j - C::kAInstr) * 8 + lr;
+            const int64_t row = kGather && isa ? source_row(a, t, t.m0 + r) : r;
+            off[j] = (uint32_t)(row * a.K + ((ls ^ swz(r)) << 4));
+        }
+    }
+};
+
+// One stage's loads.  Past the tile's last stage (live false) the resources
+// are empty and the scalar offset is 0: every load is out of range.
+template <class C, bool kGather>
+struct StageLoad {
+    __amdgpu_buffer_rsrc_t ra, rb;
+    char *buf;
+    uint32_t kbyte, tail;
+
+    __device__ __forceinline__ StageLoad(const Loader<C, kGather> &ld, char *smem, int s, int numK,
+                                         bool half)
+    {
+        const bool live = s < numK;
+        ra = resource(ld.pa, live ? ld.na : 0);
+        rb = resource(ld.pb, live ? ld.nb : 0);
+        buf = smem + s % C::STAGES * C::kStageBytes;
+        kbyte = live ? (uint32_t)s * kB128 : 0;
+        tail = half && s == numK - 1 ? ~0u : 0u;   // a last block of 64
+    }
+    // Load j of the wavefront's.
+    __device__ __forceinline__ void issue(const Loader<C, kGather> &ld, int wave, int j) const
+    {
+        const bool isa = j < C::kAInstr;
+        const int i = isa ? wave * C::kAInstr + j : C::BM / 8 + wave * C::kBInstr + j - C::kAInstr;
+        gemm::lds_load16(isa ? ra : rb, (lds_void *)(buf + i * 1024),
+                         ld.off[j] | (ld.upper[j & 1] & tail), kbyte);
+    }
+};
+
+__device__ __forceinline__ v8i read_frag(const char *p0, const char *p1)
 {
-    constexpr int kReads = C::FM + C::FN, kMfma = C::FM * C::FN;
+    const v4i lo = *reinterpret_cast<const v4i *>(p0), hi = *reinterpret_cast<const v4i *>(p1);
+    return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
+// A finished wavefront tile, out through the wavefront's own staging `st`, 16
+// rows of its kTN columns at a time, so that a store instruction fills whole
+// lines.  A lane holds 4 columns (unit u = 4j + g) of row r; the unit sits in
+// slot u ^ 2r, so that the rows write without conflicts.
+template <class C, int kT>
+__device__ __forceinline__ void store_tile(const B128Args &a, const Tile &t,
+                                           v4f (&acc)[C::FM][C::FN], char *st, int wm, int wn,
+                                           int lane)
+{
+    constexpr int kUnits = C::kTN / 4, kMask = kUnits - 1;
+    constexpr int kPieces = C::kTN / 8, kRowsPerStore = 64 / kPieces;
+    const int r = lane % 16, g = lane / 16, pc = lane % kPieces, pr = lane / kPieces;
+    const int64_t nw = t.n0 + wn * C::kTN, n = nw + 8 * pc;
+    const int m0 = t.m0 + wm * C::kTM + pr;
+    uint2 bias[C::FN];
 #pragma unroll
-    for (int m = 0; m < kMfma; ++m) {
+    for (int j = 0; j < C::FN; ++j) {
+        bias[j] = make_uint2(0, 0);
+        if (a.bias)
+            bias[j] = *reinterpret_cast<const uint2 *>(
+                a.bias + (int64_t)t.e * a.N + min(nw + j * 16 + 4 * g, a.N - 4));
+    }
+    uint16_t *out = a.out + (int64_t)m0 * a.N + n;
+    const float lowest = lowest_output(a);
 #pragma unroll
-        for (int g = m * kNL / kMfma; g < (m + 1) * kNL / kMfma; ++g)
-            ld.issue_one(smem, buf, kbyte, wave, g);
+    for (int i = 0; i < C::FM; ++i) {
 #pragma unroll
-        for (int g = (m * kReads + kMfma - 1) / kMfma; g < ((m + 1) * kReads + kMfma - 1) / kMfma; ++g)
-            gemm::read_one8<C>(nxt, sa, sb, fo0, fo1, g);
-        const int i = m / C::FN, j = m % C::FN;
-        pin(acc[i][j]);
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(cur.b[j], cur.a[i], acc[i][j],
-                                                                    0, 0, 0, sw, 0, sx[i]);
-        pin(acc[i][j]);
+        for (int j = 0; j < C::FN; ++j) {
+            pin(acc[i][j]);   // stays an accumulator register until its turn
+            *reinterpret_cast<uint2 *>(st + r * (C::kTN * 2) + 8 * ((4 * j + g) ^ (2 * r & kMask))) =
+                finish4<kT>(acc[i][j], bias[j], lowest);
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < 16; q += kRowsPerStore) {
+            const int row = q + pr;
+            const uint4 w = *reinterpret_cast<const uint4 *>(
+                st + row * (C::kTN * 2) + 16 * (pc ^ (row & (kMask >> 1))));
+            if (m0 + i * 16 + q < t.mend && n < a.N)
+                *reinterpret_cast<uint4 *>(out + (int64_t)(i * 16 + q) * a.N) = w;
+        }
+        __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-template <class C>
+template <class C, bool kGather>
 __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
 {
-    static_assert(C::ROWB == 128 && C::STAGES == 2, "one block of K per stage");
-    static_assert(C::BN / C::WN <= kB128 && kB128 % (C::BN / C::WN) == 0,
-                  "a wavefront's columns share a scale row");
-    static_assert(C::BM * C::BN * 2 <= C::kLdsBytes, "output tile fits the ring");
     __shared__ __attribute__((aligned(1024))) char smem[C::kLdsBytes];
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    Tile t;
-    if (!find_tile<C::BM, C::BN, C::GROUP>(a, lane, t))
+    Tiles<C::BM, C::BN, C::GROUP> tiles;
+    tiles.init(a, lane);
+    const int count = tiles.count();
+    int v = blockIdx.x;
+    if (v >= count)
         return;
+    Tile t = tiles.find(a, v, lane);
     const int wm = wave / C::WN, wn = wave % C::WN;
-    const int numK = (int)((a.K + kB128 - 1) / kB128), full = (int)(a.K / kB128);
+    const int r = lane % 16, g = lane / 16;
+    const int numK = (int)((a.K + kB128 - 1) / kB128);
 
-    BigLoads<C> ld;
-    ld.init(a, t, wave, lane);
-
-    // scales: this lane's rows and its wavefront's columns
+    // Scales: chunk c of the tile into its buffer, 16 bytes of one row per lane
+    // and, a dword per lane, those of the wavefront's columns.  Rows, and
+    // bytes past a row's end, that no output needs hold anything.
     const int64_t pitch = b128_pitch(a.K);
-    const int64_t xr = x_base_row(a, t);
-    const __amdgpu_buffer_rsrc_t rsx = resource(a.SX + xr * pitch, (a.rows - xr) * pitch);
-    const int64_t ws = min(t.n0 + wn * (C::BN / C::WN), a.N - 1) / kB128;
-    const __amdgpu_buffer_rsrc_t rsw =
-        resource(a.SB + ((int64_t)t.e * scale_rows(a) + ws) * pitch, pitch);
-    uint32_t soff[C::FM];
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i)
-        soff[i] = (uint32_t)(
-            (source_row(a, t, t.m0 + wm * (C::BM / C::WM) + i * 32 + lane % 32) - xr) * pitch);
-    unsigned sx[C::FM], sxn[C::FM], sw, swn;
-    auto load_scales = [&](unsigned(&x)[C::FM], unsigned &w, int kt) {
-        const uint32_t g = (uint32_t)(kt < numK ? kt : numK - 1) / 4 * 4;
+    __amdgpu_buffer_rsrc_t rsx, rsw;
+    uint32_t soff;
+    auto scale_rows_of = [&](const Tile &q) {
+        const int64_t xr = kGather ? 0 : q.m0;
+        rsx = resource(a.SX + xr * pitch, ((kGather ? a.rows : q.mend) - xr) * pitch);
+        const int64_t n = min(q.n0 + wn * C::kTN, a.N - 1) / kB128;
+        rsw = resource(a.SB + ((int64_t)q.e * scale_rows(a) + n) * pitch, pitch);
+        const int row = tid % C::BM;
+        soff = (uint32_t)((kGather ? source_row(a, q, q.m0 + row) : row) * pitch);
+    };
+    auto load_scales = [&](int c) {
+        char *sc = smem + C::kRing + (c & 1) * C::kScaleBytes;
+        if (wave * 64 < C::BM)
+            gemm::lds_load16(rsx, (lds_void *)(sc + wave * 1024), soff, (uint32_t)c * C::kChunk);
+        lds_load4(rsw, (lds_void *)(sc + C::kScaleRows + wave * 256), lane % 4 * 4,
+                  (uint32_t)c * C::kChunk);
+    };
+    const int nchunk = (numK + C::kChunk - 1) / C::kChunk;
+    unsigned sx[C::FM], sw;
+    auto read_scales = [&](int kt) {
+        const uint8_t *sc = reinterpret_cast<const uint8_t *>(smem) + C::kRing +
+                            (kt / C::kChunk & 1) * C::kScaleBytes + kt % C::kChunk;
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
-            x[i] = buf_load4(rsx, soff[i], g);
-        w = buf_load4(rsw, 0, g);
+            sx[i] = sc[(wm * C::kTM + i * 16 + r) * C::kChunk];
+        sw = sc[C::kScaleRows + wave * 256];
     };
 
-    v16f acc[C::FM][C::FN];
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-                acc[i][j][q] = 0;
-
-    const int frow = (lane & 31) * C::ROWB, h = lane >> 5, swz = C::swz(lane & 31);
-    int fo0[2], fo1[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        fo0[s] = frow + (((4 * s + h) ^ swz) << 4);
-        fo1[s] = frow + (((4 * s + 2 + h) ^ swz) << 4);
-    }
-    const int aoff = wm * (C::BM / C::WM) * C::ROWB;
-    const int boff = C::BM * C::ROWB + wn * (C::BN / C::WN) * C::ROWB;
-    auto kbyte = [&](int s) { return (uint32_t)(s < numK ? s : numK - 1) * C::ROWB; };
-
-    load_scales(sx, sw, 0);
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
+    Loader<C, kGather> ld;
+    const bool half = a.K % kB128 != 0;
+    auto load_stage = [&](int s) {
+        const StageLoad<C, kGather> sl(ld, smem, s, numK, half);
 #pragma unroll
         for (int j = 0; j < C::kLoads; ++j)
-            ld.issue_one(smem, s, kbyte(s), wave, j);
-    wait_vm<C::kLoads>();   // stage 0 (and the scales, loaded before it)
-    __builtin_amdgcn_s_barrier();
+            sl.issue(ld, wave, j);
+    };
+    // a tile's first scales and stages
+    auto start = [&]() {
+        scale_rows_of(t);
+        load_scales(0);
+        ld.init(a, t, wave, lane);
+#pragma unroll 1
+        for (int s = 0; s < C::STAGES; ++s)
+            load_stage(s);
+    };
+    start();
 
-    // The loop of gemm::mainloop_f8: fragments one k-step ahead, one barrier
-    // per stage before its last k-step, under which the stage's buffer is
-    // refilled with the stage after the next.
-    gemm::Frags8<C> f0, f1;
-#pragma unroll
-    for (int q = 0; q < C::FM + C::FN; ++q)
-        gemm::read_one8<C>(f0, smem + aoff, smem + boff, fo0[0], fo1[0], q);
-    for (int kt = 0; kt < full; ++kt) {
-        const char *cs = smem + (kt & 1) * C::kStageBytes;
-        const char *ns = smem + (kt + 1 < numK ? (kt + 1) & 1 : kt & 1) * C::kStageBytes;
-        kstep<C, 0>(f0, f1, cs + aoff, cs + boff, fo0[1], fo1[1], acc, sx, sw, ld, smem, 0, 0, wave);
-        wait_vm<0>();   // stage kt + 1 has landed, and the scales on their way
-        __builtin_amdgcn_s_barrier();
-        if ((kt & 3) == 0)
-            load_scales(sxn, swn, kt + 4);
-        kstep<C, C::kLoads>(f1, f0, ns + aoff, ns + boff, fo0[0], fo1[0], acc, sx, sw, ld, smem,
-                            kt & 1, kbyte(kt + 2), wave);
-        const bool next = (kt & 3) == 3;
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-            sx[i] = next ? sxn[i] : sx[i] >> 8;
-        sw = next ? swn : sw >> 8;
-    }
-    if (full < numK) {   // a last block of 64: its first k-step, already in f0
+    v4f acc[C::FM][C::FN];
+    v8i fa[C::FM], fb[C::FN];
+    const int fo0 = r * 128 + ((g ^ swz(r)) << 4), fo1 = r * 128 + (((g + 4) ^ swz(r)) << 4);
+    const int aoff = wm * C::kTM * 128, boff = (C::BM + wn * C::kTN) * 128;
+    auto read_a = [&](const char *buf, int i) {
+        fa[i] = read_frag(buf + aoff + i * 2048 + fo0, buf + aoff + i * 2048 + fo1);
+    };
+    auto read_b = [&](const char *buf, int j) {
+        fb[j] = read_frag(buf + boff + j * 2048 + fo0, buf + boff + j * 2048 + fo1);
+    };
+
+    for (;;) {
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
 #pragma unroll
             for (int j = 0; j < C::FN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    f0.b[j], f0.a[i], acc[i][j], 0, 0, 0, sw, 0, sx[i]);
-    }
-    wait_vm<0>();      // the tail loads have landed
-    __syncthreads();   // and nobody reads the ring any more
-
-    // The finished tile goes out through LDS in whole lines (a lane holds 4
-    // columns of one row at a time): 8-byte unit u of row r sits in slot
-    // u ^ (r & mask), so that the rows of a tile write without conflicts.
-    constexpr int kUnits = C::BN / 4, kMask = kUnits < 32 ? kUnits - 1 : 31;
-    const int tl = lane & 31;
+                acc[i][j] = v4f{0, 0, 0, 0};
+        // the first stage and scales have landed; its fragments, but for A's last pair
+        wait_vm<(C::STAGES - 1) * C::kLoads>();
+        __builtin_amdgcn_s_barrier();
+        read_scales(0);
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
+        for (int i = 0; i < C::FM - 2; ++i)
+            read_a(smem, i);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int c = wn * (C::BN / C::WN) + j * 32 + 8 * q + 4 * h;   // column in the tile
-            uint2 b = make_uint2(0, 0);
-            if (a.bias) {
-                const int64_t n = t.n0 + c < a.N ? t.n0 + c : a.N - 4;
-                b = *reinterpret_cast<const uint2 *>(a.bias + (int64_t)t.e * a.N + n);
+        for (int j = 0; j < C::FN; ++j)
+            read_b(smem, j);
+        for (int kt = 0; kt < numK; ++kt) {
+            const char *cbuf = smem + kt % C::STAGES * C::kStageBytes;
+            const char *nbuf = smem + (kt + 1) % C::STAGES * C::kStageBytes;
+            const StageLoad<C, kGather> sl(ld, smem, kt + C::STAGES, numK, half);
+            // the other chunk's last bytes were read before the last barrier
+            if (kt % C::kChunk == 0 && kt / C::kChunk + 1 < nchunk)
+                load_scales(kt / C::kChunk + 1);
+#pragma unroll
+            for (int m = 0; m < C::FM * C::FN; ++m) {
+                const int p = m / (2 * C::FN), w = m % (2 * C::FN);   // pair, place in it
+                const int i = 2 * p + w % 2, j = w / 2;
+                if (m == 0)
+                    read_a(cbuf, C::FM - 2);
+                if (m == 2)
+                    read_a(cbuf, C::FM - 1);
+                if (m == 2 * C::FN) {
+                    // all reads of this stage are done and the next stage has
+                    // landed, for this wavefront, then for all
+                    gemm::wait_lds();
+                    wait_vm<(C::STAGES - 2) * C::kLoads>();
+                    __builtin_amdgcn_s_barrier();
+                }
+                if (m >= 2 * C::FN && m - 2 * C::FN < C::kLoads)
+                    sl.issue(ld, wave, m - 2 * C::FN);
+                if (p > 0 && (w == 0 || w == 2))
+                    read_a(nbuf, 2 * p - 2 + w / 2);
+                if (p == C::FM / 2 - 1 && w >= 2 && w % 2 == 0)
+                    read_b(nbuf, j - 1);
+                pin(acc[i][j]);
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    fb[j], fa[i], acc[i][j], 0, 0, 0, sw, 0, sx[i]);
+                pin(acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-            for (int i = 0; i < C::FM; ++i) {
-                const int row = wm * (C::BM / C::WM) + i * 32 + tl;
-                const v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                               acc[i][j][4 * q + 3]};
-                const uint2 o = a.type == kTypeBf16
-                                    ? finish4<kTypeBf16>(v, a.bias != nullptr, b, a.act)
-                                    : finish4<kTypeF16>(v, a.bias != nullptr, b, a.act);
-                *reinterpret_cast<uint2 *>(smem + row * (C::BN * 2) +
-                                           8 * ((c / 4) ^ (row & kMask))) = o;
-            }
+            read_b(nbuf, C::FN - 1);
+            read_scales(kt + 1);
         }
-    }
-    __syncthreads();
-    constexpr int kPieces = C::BN / 8, kRowsPerPass = C::kThreads / kPieces;
-    const int p = tid % kPieces;
-#pragma unroll 4
-    for (int r = tid / kPieces; r < C::BM; r += kRowsPerPass) {
-        uint4 v = *reinterpret_cast<const uint4 *>(smem + r * (C::BN * 2) +
-                                                   16 * (p ^ ((r & kMask) >> 1)));
-        if (r & 1)
-            v = make_uint4(v.z, v.w, v.x, v.y);
-        const int64_t n = t.n0 + 8 * p;
-        if (t.m0 + r < t.mend && n < a.N)
-            *reinterpret_cast<uint4 *>(a.out + (int64_t)(t.m0 + r) * a.N + n) = v;
+        const Tile done = t;
+        v += gridDim.x;
+        wait_vm<0>();      // the loads past the end have landed,
+        __syncthreads();   // and nobody reads the ring any more
+        if (v < count) {
+            t = tiles.find(a, v, lane);
+            start();
+        }
+        if (a.type == kTypeBf16)
+            store_tile<C, kTypeBf16>(a, done, acc, smem + C::kRing + wave * C::kOutBytes, wm, wn,
+                                     lane);
+        else
+            store_tile<C, kTypeF16>(a, done, acc, smem + C::kRing + wave * C::kOutBytes, wm, wn,
+                                    lane);
+        if (v >= count)
+            break;
     }
 }
 
+// The most tiles a launch may have: at most M / BM whole tile rows and a ragged
+// one per expert.
 template <class C>
-hipError_t launch_tiles(void (*kernel)(B128Args), const B128Args &a, hipStream_t s)
+int64_t most_tiles(const B128Args &a)
 {
     const int64_t ntn = (a.N + C::BN - 1) / C::BN;
-    // at most M / BM whole tiles and a ragged one per expert
-    const int64_t ntm = a.offsets ? a.M / C::BM + (a.E < a.M ? a.E : a.M) : (a.M + C::BM - 1) / C::BM;
-    if (ntm * ntn * C::kThreads > 0xffffffffll)
+    return ntn * (a.offsets ? a.M / C::BM + (a.E < a.M ? a.E : a.M) : (a.M + C::BM - 1) / C::BM);
+}
+
+template <class C>
+hipError_t launch_small(const B128Args &a, hipStream_t s)
+{
+    const int64_t n = most_tiles<C>(a);
+    if (n * C::kThreads > 0xffffffffll)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(ntm * ntn)), dim3(C::kThreads), 0, s, a);
+    hipLaunchKernelGGL(k_b128_small<C>, dim3((unsigned)n), dim3(C::kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+template <class C>
+hipError_t launch_big(const B128Args &a, hipStream_t s)
+{
+    constexpr int64_t kResident = 256 * C::kPerCu;
+    const int64_t n = most_tiles<C>(a);
+    if (n > 0x7fffffff)
+        return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(n < kResident ? n : kResident));
+    if (a.row_idx)
+        hipLaunchKernelGGL((k_b128_big<C, true>), grid, dim3(C::kThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_b128_big<C, false>), grid, dim3(C::kThreads), 0, s, a);
     return hipGetLastError();
 }
 
