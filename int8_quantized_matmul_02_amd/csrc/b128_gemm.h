@@ -387,10 +387,14 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
 // MFMAs go by pairs of row tiles, column by column, and the fragments of
 // stage s + 1 are read from LDS into the registers of stage s as these come
 // free: A's tiles after their pair, B's column tiles one after another during
-// the last pair (the last pair's A tiles at the start of the next stage).  By
-// the time the first pair is through, all reads of a stage are long done: the
-// one barrier of a stage sits there, and behind it stage s + STAGES is loaded
-// into the buffer that s has left.
+// the last pair (the last pair's A tiles at the start of the next stage).  Two
+// barriers per stage: after kFree MFMAs all wavefronts have read stage s, and
+// stage s + STAGES goes into its buffer, a load every kStep MFMAs (issued
+// faster, the loads stall in the address unit and the MFMAs behind them);
+// after kLand MFMAs stage s + 1 has landed.  Measured at 4096 x 4096 x 16384,
+// 4096 x 16384 x 4096 and 8192^3: one barrier after the first pair and a load
+// per MFMA 220, 218, 405 us; a load every 2nd 215, 207, 394; two barriers and
+// every 2nd 210, 204, 386; every 3rd 208, 195, 377.
 //
 // Blocks are persistent: a block takes tiles v, v + grid, ..., and loads the
 // next tile's first stages before it writes a finished tile out.  Past a
@@ -424,9 +428,18 @@ struct BigCfg {
     static constexpr int kOut = kRing + 2 * kScaleBytes;
     static constexpr int kLdsBytes = kOut + kWaves * kOutBytes;
     static constexpr int kPerCu = 160 * 1024 / kLdsBytes;      // resident blocks per CU
+    // the stage's schedule, in MFMAs
+    static constexpr int kMfmas = FM * FN, kPair = 2 * FN, kPairs = FM / 2;
+    static constexpr int kFree = kMfmas >= 64 ? 6 : 4;
+    static constexpr int kLand = kPairs > 2 ? kMfmas * 5 / 8 : kMfmas / 2;
+    static constexpr int kStep = (kMfmas - kFree) / kLoads;
+    static constexpr int kBefore = (kLand - kFree + kStep - 1) / kStep;   // loads issued before kLand
+    static_assert(kStep >= 1 && kBefore <= kLoads, "issue slots");
+    static_assert(kLand >= (kPairs - 2) * kPair && kLand + 4 * (kPairs - 2) <= (kPairs - 1) * kPair,
+                  "A's tiles are free, and read, in time");
     static_assert(BM % (8 * kWaves) == 0 && BN % (16 * kWaves) == 0, "load split");
     static_assert(kTN <= kB128 && kB128 % kTN == 0, "a wavefront's columns share a scale row");
-    static_assert(FM >= 4 && FM % 2 == 0 && kLoads <= (FM - 2) * FN, "issue slots");
+    static_assert(FM >= 4 && FM % 2 == 0, "pairs");
     static_assert(STAGES >= 2 && (STAGES - 1) * kLoads < 64, "vmcnt range");
     static_assert(kPerCu >= 1, "LDS");
     static_assert(BM == 64 * kWaves || BM == 32 * kWaves, "scales: a row per lane");
@@ -656,25 +669,30 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
             if (kt % C::kChunk == 0 && kt / C::kChunk + 1 < nchunk)
                 load_scales(kt / C::kChunk + 1);
 #pragma unroll
-            for (int m = 0; m < C::FM * C::FN; ++m) {
-                const int p = m / (2 * C::FN), w = m % (2 * C::FN);   // pair, place in it
+            for (int m = 0; m < C::kMfmas; ++m) {
+                const int p = m / C::kPair, w = m % C::kPair;   // pair, place in it
                 const int i = 2 * p + w % 2, j = w / 2;
                 if (m == 0)
                     read_a(cbuf, C::FM - 2);
                 if (m == 2)
                     read_a(cbuf, C::FM - 1);
-                if (m == 2 * C::FN) {
-                    // all reads of this stage are done and the next stage has
-                    // landed, for this wavefront, then for all
+                if (m == C::kFree) {   // every wavefront has read all of this stage
                     gemm::wait_lds();
-                    wait_vm<(C::STAGES - 2) * C::kLoads>();
                     __builtin_amdgcn_s_barrier();
                 }
-                if (m >= 2 * C::FN && m - 2 * C::FN < C::kLoads)
-                    sl.issue(ld, wave, m - 2 * C::FN);
-                if (p > 0 && (w == 0 || w == 2))
-                    read_a(nbuf, 2 * p - 2 + w / 2);
-                if (p == C::FM / 2 - 1 && w >= 2 && w % 2 == 0)
+                if (m == C::kLand) {   // the next stage has landed for every wavefront
+                    wait_vm<(C::STAGES - 2) * C::kLoads + C::kBefore>();
+                    __builtin_amdgcn_s_barrier();
+                }
+                if (m >= C::kFree && (m - C::kFree) % C::kStep == 0 &&
+                    (m - C::kFree) / C::kStep < C::kLoads)
+                    sl.issue(ld, wave, (m - C::kFree) / C::kStep);
+                if (m >= C::kLand && (m - C::kLand) % 2 == 0 &&
+                    (m - C::kLand) / 2 < 2 * (C::kPairs - 2))
+                    read_a(nbuf, (m - C::kLand) / 2);
+                if (p == C::kPairs - 1 && (w == 0 || w == 2))
+                    read_a(nbuf, C::FM - 4 + w / 2);
+                if (p == C::kPairs - 1 && w >= 2 && w % 2 == 0)
                     read_b(nbuf, j - 1);
                 pin(acc[i][j]);
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
