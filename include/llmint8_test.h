@@ -101,6 +101,24 @@ LLMINT8_API llmint8_status_t llmint8_mfma_ceiling(const void *A, int64_t T, cons
                                                   int iters, int32_t *out, hipEvent_t start,
                                                   hipEvent_t stop, hipStream_t stream);
 
+/*
+ * llmint8_matmul_b128 and llmint8_matmul_grouped_b128 with the kernel chosen:
+ * path 1 .. 7 forces a tile of 16 x 16, 16 x 32, 32 x 32, 64 x 64, 64 x 128, 128 x 128
+ * or 256 x 256 outputs, 0 leaves the choice; parts 1 .. 8 forces into how many
+ * parts K is split (fewer if it has fewer groups of 512 columns), 0 leaves the
+ * choice.  Others -> LLMINT8_ERR_INVALID_ARG.
+ */
+LLMINT8_API size_t llmint8_matmul_b128_workspace_bytes_path(int64_t T, int64_t K, int64_t N,
+                                                            int path, int parts);
+LLMINT8_API llmint8_status_t llmint8_matmul_b128_path(
+    const uint8_t *Xq8, const uint8_t *SX, int64_t T, int64_t K, int64_t N, const uint8_t *CB8,
+    const uint8_t *SB, const uint16_t *bias, int activation, int type, uint16_t *out, void *ws,
+    size_t ws_bytes, int path, int parts, hipStream_t stream);
+LLMINT8_API llmint8_status_t llmint8_matmul_grouped_b128_path(
+    const uint8_t *Xq8, const uint8_t *SX, int64_t T, int64_t K, int64_t N, const uint8_t *CB8,
+    const uint8_t *SB, int64_t E, const int32_t *offsets, const int32_t *row_idx, int64_t M,
+    const uint16_t *bias, int activation, int type, uint16_t *out, int path, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

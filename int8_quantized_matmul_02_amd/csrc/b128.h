@@ -98,8 +98,15 @@ struct B128Args {
     int E = 1;
     const int32_t *offsets = nullptr;
     const int32_t *row_idx = nullptr;
+    // A plain product may split K: part p takes `per` blocks of K from p * per
+    // on and writes fp32 sums to parts [parts, M, N] instead of out.
+    int nparts = 1, per = 0;
+    float *parts = nullptr;
 };
-hipError_t launch_matmul_b128(const B128Args &a, void *ws, hipStream_t s);
-size_t b128_workspace_bytes(int64_t T, int64_t K, int64_t N);
+// path: 0, or one of the kernel shapes 1 .. kB128Paths; parts: 0, or into how
+// many parts K is split (1 for a grouped product); both 0: the estimate's choice.
+constexpr int kB128Paths = 7, kB128MostParts = 8;
+hipError_t launch_matmul_b128(const B128Args &a, void *ws, int path, int parts, hipStream_t s);
+size_t b128_workspace_bytes(int64_t T, int64_t K, int64_t N, int path, int parts);
 
 }  // namespace llmint8

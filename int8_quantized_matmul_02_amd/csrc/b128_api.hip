@@ -3,7 +3,7 @@
 
 #include <math.h>
 
-#include "../../include/llmint8.h"
+#include "../../include/llmint8_test.h"
 #include "b128.h"
 
 using namespace llmint8;
@@ -15,6 +15,11 @@ bool aligned8(const void *p) { return ((uintptr_t)p & 7u) == 0; }
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 bool bad_type(int t) { return t != LLMINT8_F16 && t != LLMINT8_BF16; }
 bool bad_act(int a) { return a != LLMINT8_ACT_NONE && a != LLMINT8_ACT_RELU; }
+
+bool bad_path(int path, int parts)
+{
+    return path < 0 || path > kB128Paths || parts < 0 || parts > kB128MostParts;
+}
 
 // Sizes the kernels index in 32 bits.
 constexpr int64_t kMaxRows = 0x7fff0000;
@@ -96,11 +101,40 @@ llmint8_status_t llmint8_quantize_weight_b128(const uint16_t *W_t, int type, int
     return status(launch_quantize_weight_b128(W_t, E, N, K, type, CB8, SB, stream));
 }
 
+size_t llmint8_matmul_b128_workspace_bytes_path(int64_t T, int64_t K, int64_t N, int path,
+                                                int parts)
+{
+    return check_b128(T, K, N, 1) == LLMINT8_OK && T * N <= kMaxOutputs && !bad_path(path, parts)
+               ? b128_workspace_bytes(T, K, N, path, parts)
+               : 0;
+}
+
 size_t llmint8_matmul_b128_workspace_bytes(int64_t T, int64_t K, int64_t N)
 {
-    return check_b128(T, K, N, 1) == LLMINT8_OK && T * N <= kMaxOutputs
-               ? b128_workspace_bytes(T, K, N)
-               : 0;
+    return llmint8_matmul_b128_workspace_bytes_path(T, K, N, 0, 0);
+}
+
+llmint8_status_t llmint8_matmul_b128_path(const uint8_t *Xq8, const uint8_t *SX, int64_t T,
+                                          int64_t K, int64_t N, const uint8_t *CB8,
+                                          const uint8_t *SB, const uint16_t *bias, int activation,
+                                          int type, uint16_t *out, void *ws, size_t ws_bytes,
+                                          int path, int parts, hipStream_t stream)
+{
+    if (!Xq8 || !SX || !CB8 || !SB || !out || !aligned16(Xq8) || !aligned4(SX) ||
+        !aligned16(CB8) || !aligned4(SB) || !aligned8(bias) || !aligned16(out) ||
+        !aligned16(ws) || bad_act(activation) || bad_type(type) || bad_path(path, parts))
+        return LLMINT8_ERR_INVALID_ARG;
+    const llmint8_status_t st = check_b128(T, K, N, 1);
+    if (st != LLMINT8_OK)
+        return st;
+    if (T * N > kMaxOutputs)
+        return LLMINT8_ERR_UNSUPPORTED_SHAPE;
+    const size_t need = b128_workspace_bytes(T, K, N, path, parts);
+    if (need && (!ws || ws_bytes < need))
+        return LLMINT8_ERR_WORKSPACE;
+    return status(launch_matmul_b128(
+        B128Args{Xq8, SX, CB8, SB, bias, out, T, T, K, N, activation, type}, ws, path, parts,
+        stream));
 }
 
 llmint8_status_t llmint8_matmul_b128(const uint8_t *Xq8, const uint8_t *SX, int64_t T, int64_t K,
@@ -108,32 +142,22 @@ llmint8_status_t llmint8_matmul_b128(const uint8_t *Xq8, const uint8_t *SX, int6
                                      const uint16_t *bias, int activation, int type,
                                      uint16_t *out, void *ws, size_t ws_bytes, hipStream_t stream)
 {
-    if (!Xq8 || !SX || !CB8 || !SB || !out || !aligned16(Xq8) || !aligned4(SX) ||
-        !aligned16(CB8) || !aligned4(SB) || !aligned8(bias) || !aligned16(out) ||
-        !aligned16(ws) || bad_act(activation) || bad_type(type))
-        return LLMINT8_ERR_INVALID_ARG;
-    const llmint8_status_t st = check_b128(T, K, N, 1);
-    if (st != LLMINT8_OK)
-        return st;
-    if (T * N > kMaxOutputs)
-        return LLMINT8_ERR_UNSUPPORTED_SHAPE;
-    const size_t need = b128_workspace_bytes(T, K, N);
-    if (need && (!ws || ws_bytes < need))
-        return LLMINT8_ERR_WORKSPACE;
-    return status(launch_matmul_b128(
-        B128Args{Xq8, SX, CB8, SB, bias, out, T, T, K, N, activation, type}, ws, stream));
+    return llmint8_matmul_b128_path(Xq8, SX, T, K, N, CB8, SB, bias, activation, type, out, ws,
+                                    ws_bytes, 0, 0, stream);
 }
 
-llmint8_status_t llmint8_matmul_grouped_b128(const uint8_t *Xq8, const uint8_t *SX, int64_t T,
-                                             int64_t K, int64_t N, const uint8_t *CB8,
-                                             const uint8_t *SB, int64_t E,
-                                             const int32_t *offsets, const int32_t *row_idx,
-                                             int64_t M, const uint16_t *bias, int activation,
-                                             int type, uint16_t *out, hipStream_t stream)
+llmint8_status_t llmint8_matmul_grouped_b128_path(const uint8_t *Xq8, const uint8_t *SX, int64_t T,
+                                                  int64_t K, int64_t N, const uint8_t *CB8,
+                                                  const uint8_t *SB, int64_t E,
+                                                  const int32_t *offsets, const int32_t *row_idx,
+                                                  int64_t M, const uint16_t *bias, int activation,
+                                                  int type, uint16_t *out, int path,
+                                                  hipStream_t stream)
 {
     if (!Xq8 || !SX || !CB8 || !SB || !offsets || !out || !aligned16(Xq8) || !aligned4(SX) ||
         !aligned16(CB8) || !aligned4(SB) || !aligned4(offsets) || !aligned4(row_idx) ||
-        !aligned8(bias) || !aligned16(out) || bad_act(activation) || bad_type(type) || M <= 0 ||
+        !aligned8(bias) || !aligned16(out) || bad_act(activation) || bad_type(type) ||
+        bad_path(path, 1) || M <= 0 ||
         (!row_idx && M != T))
         return LLMINT8_ERR_INVALID_ARG;
     const llmint8_status_t st = check_b128(T, K, N, E);
@@ -144,7 +168,18 @@ llmint8_status_t llmint8_matmul_grouped_b128(const uint8_t *Xq8, const uint8_t *
         return LLMINT8_ERR_UNSUPPORTED_SHAPE;
     return status(launch_matmul_b128(B128Args{Xq8, SX, CB8, SB, bias, out, T, M, K, N, activation,
                                               type, (int)E, offsets, row_idx},
-                                     nullptr, stream));
+                                     nullptr, path, 1, stream));
+}
+
+llmint8_status_t llmint8_matmul_grouped_b128(const uint8_t *Xq8, const uint8_t *SX, int64_t T,
+                                             int64_t K, int64_t N, const uint8_t *CB8,
+                                             const uint8_t *SB, int64_t E,
+                                             const int32_t *offsets, const int32_t *row_idx,
+                                             int64_t M, const uint16_t *bias, int activation,
+                                             int type, uint16_t *out, hipStream_t stream)
+{
+    return llmint8_matmul_grouped_b128_path(Xq8, SX, T, K, N, CB8, SB, E, offsets, row_idx, M,
+                                            bias, activation, type, out, 0, stream);
 }
 
 }  // extern "C"

@@ -41,6 +41,7 @@ struct Tile {
     int e;            // expert
     int m0, mend;     // first output row, end of the expert's rows
     int64_t n0;
+    int k0, nk;       // first block of K and their number
 };
 
 // Rows of 64 experts from `base` on: each lane's bounds, kept inside [0, M]
@@ -94,16 +95,19 @@ struct Tiles {
                                              kWave - 1);
         }
     }
-    __device__ __forceinline__ int count() const { return ntm * ntn; }
+    __device__ __forceinline__ int count(const B128Args &a) const { return ntm * ntn * a.nparts; }
 
-    // Tile v < count(): workgroup ids are dealt round-robin over the XCDs, so
+    // Tile v < count(), the parts of K one after another: workgroup ids are dealt round-robin over the XCDs, so
     // each XCD takes a contiguous run of tiles, which walk GROUP tile rows at
     // a time.
     __device__ __forceinline__ Tile find(const B128Args &a, int v, int lane) const
     {
         Tile t;
         int tm, tn;
-        gemm::tile_coords(v, ntm * ntn, ntm, ntn, GROUP, tm, tn);
+        const int part = a.nparts > 1 ? v / (ntm * ntn) : 0;
+        gemm::tile_coords(v - part * (ntm * ntn), ntm * ntn, ntm, ntn, GROUP, tm, tn);
+        t.k0 = part * a.per;
+        t.nk = min((int)((a.K + kB128 - 1) / kB128) - t.k0, a.nparts > 1 ? a.per : INT32_MAX);
         t.n0 = (int64_t)tn * BN;
         t.e = 0;
         t.m0 = tm * BM;
@@ -241,12 +245,12 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     Tiles<C::BM, C::BN, C::GROUP> tiles;
     tiles.init(a, lane);
-    if ((int)blockIdx.x >= tiles.count())
+    if ((int)blockIdx.x >= tiles.count(a))
         return;
     const Tile t = tiles.find(a, blockIdx.x, lane);
     const int wn = wave % C::WN, wm = wave / C::WN % C::WM, wk = wave / (C::WN * C::WM);
     const int64_t pitch = b128_pitch(a.K);
-    const int nblk = (int)((a.K + kB128 - 1) / kB128), nst = (nblk + 3) / 4;
+    const int nst = (t.nk + 3) / 4;   // stages of four blocks
 
     // loads: instruction j of the block's fills staged rows 2j and 2j + 1 (the
     // activations' first)
@@ -278,10 +282,10 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
         for (int u = 0; u < C::kInstr; ++u) {
             const int j = wave * C::kInstr + u;
             gemm::lds_load16(2 * j < C::BM ? rx : rw, (lds_void *)(st + j * 1024), off[u],
-                             (uint32_t)sc * C::kRowB);
+                             (uint32_t)(t.k0 * kB128 + sc * C::kRowB));
         }
         lds_load4(xs ? rsx : rsw, (lds_void *)(st + (C::BM + C::BN) * C::kRowB + wave * 256), soff,
-                  (uint32_t)sc * 4);
+                  (uint32_t)(t.k0 + sc * 4));
     };
 
     v4f acc[C::FM][C::FN];
@@ -321,8 +325,8 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
 #pragma unroll
         for (int b = 0; b < C::kBlocks; ++b) {
             const int blk = C::kBlocks * wk + b;
-            if (4 * kt + blk < nblk) {
-                const bool half = (int64_t)(4 * kt + blk) * kB128 + 64 == a.K;
+            if (4 * kt + blk < t.nk) {
+                const bool half = (int64_t)(t.k0 + 4 * kt + blk) * kB128 + 64 == a.K;
                 v8i fa[C::FM], fb[C::FN];
 #pragma unroll
                 for (int i = 0; i < C::FM; ++i)
@@ -363,8 +367,10 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
         for (int w = 1; w < C::WK; ++w)
             v += *reinterpret_cast<const v4f *>(sums + (w * C::BM + row) * C::kSumPitch + c);
         const int64_t n = t.n0 + c;
-        if (n >= a.N)
+        if (a.parts) {
+            *reinterpret_cast<v4f *>(a.parts + ((t.k0 / a.per) * a.M + t.m0 + row) * a.N + n) = v;
             continue;
+        }
         uint2 b = make_uint2(0, 0);
         if (a.bias)
             b = *reinterpret_cast<const uint2 *>(a.bias + (int64_t)t.e * a.N + n);
@@ -389,7 +395,7 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
 // free: A's tiles after their pair, B's column tiles one after another during
 // the last pair (the last pair's A tiles at the start of the next stage).  Two
 // barriers per stage: after kFree MFMAs all wavefronts have read stage s, and
-// stage s + STAGES goes into its buffer, a load every kStep MFMAs (issued
+// stage s + STAGES goes into its buffer, spread over the rest (issued
 // faster, the loads stall in the address unit and the MFMAs behind them);
 // after kLand MFMAs stage s + 1 has landed.  Measured at 4096 x 4096 x 16384,
 // 4096 x 16384 x 4096 and 8192^3: one barrier after the first pair and a load
@@ -430,11 +436,20 @@ struct BigCfg {
     static constexpr int kPerCu = 160 * 1024 / kLdsBytes;      // resident blocks per CU
     // the stage's schedule, in MFMAs
     static constexpr int kMfmas = FM * FN, kPair = 2 * FN, kPairs = FM / 2;
-    static constexpr int kFree = kMfmas >= 64 ? 6 : 4;
+    static constexpr int kFree = kMfmas >= 64 ? 6 : kMfmas >= 16 ? 4 : 3;
     static constexpr int kLand = kPairs > 2 ? kMfmas * 5 / 8 : kMfmas / 2;
-    static constexpr int kStep = (kMfmas - kFree) / kLoads;
-    static constexpr int kBefore = (kLand - kFree + kStep - 1) / kStep;   // loads issued before kLand
-    static_assert(kStep >= 1 && kBefore <= kLoads, "issue slots");
+    static constexpr int slot(int load)   // the MFMA before which a stage load is issued
+    {
+        const int room = kMfmas - kFree, step = room / kLoads;
+        return kFree + (step >= 1 ? load * step : load * room / kLoads);
+    }
+    static constexpr int before(int m)    // loads issued before MFMA m
+    {
+        int n = 0;
+        for (int j = 0; j < kLoads; ++j)
+            n += slot(j) < m;
+        return n;
+    }
     static_assert(kLand >= (kPairs - 2) * kPair && kLand + 4 * (kPairs - 2) <= (kPairs - 1) * kPair,
                   "A's tiles are free, and read, in time");
     static_assert(BM % (8 * kWaves) == 0 && BN % (16 * kWaves) == 0, "load split");
@@ -442,7 +457,7 @@ struct BigCfg {
     static_assert(FM >= 4 && FM % 2 == 0, "pairs");
     static_assert(STAGES >= 2 && (STAGES - 1) * kLoads < 64, "vmcnt range");
     static_assert(kPerCu >= 1, "LDS");
-    static_assert(BM == 64 * kWaves || BM == 32 * kWaves, "scales: a row per lane");
+    static_assert(BM % 64 == 0 && BM <= 64 * kWaves, "scales: a row per lane");
 };
 
 // Keeps the MFMAs on `v` between the side-effecting operations around this
@@ -495,15 +510,16 @@ struct StageLoad {
     char *buf;
     uint32_t kbyte, tail;
 
-    __device__ __forceinline__ StageLoad(const Loader<C, kGather> &ld, char *smem, int s, int numK,
-                                         bool half)
+    // s: the stage within the tile; last: the block of K that has 64 columns, or -1.
+    __device__ __forceinline__ StageLoad(const Loader<C, kGather> &ld, char *smem, const Tile &t,
+                                         int s, int last)
     {
-        const bool live = s < numK;
+        const bool live = s < t.nk;
         ra = resource(ld.pa, live ? ld.na : 0);
         rb = resource(ld.pb, live ? ld.nb : 0);
         buf = smem + s % C::STAGES * C::kStageBytes;
-        kbyte = live ? (uint32_t)s * kB128 : 0;
-        tail = half && s == numK - 1 ? ~0u : 0u;   // a last block of 64
+        kbyte = live ? (uint32_t)(t.k0 + s) * kB128 : 0;
+        tail = t.k0 + s == last ? ~0u : 0u;
     }
     // Load j of the wavefront's.
     __device__ __forceinline__ void issue(const Loader<C, kGather> &ld, int wave, int j) const
@@ -566,6 +582,26 @@ __device__ __forceinline__ void store_tile(const B128Args &a, const Tile &t,
     }
 }
 
+// One part's sums of a wavefront tile: 16 bytes per lane, 64 of a row together.
+template <class C>
+__device__ __forceinline__ void store_parts(const B128Args &a, const Tile &t,
+                                            v4f (&acc)[C::FM][C::FN], int wm, int wn, int lane)
+{
+    const int64_t n = t.n0 + wn * C::kTN + 4 * (lane / 16);
+    const int m0 = t.m0 + wm * C::kTM + lane % 16;
+    float *out = a.parts + ((t.k0 / a.per) * a.M + m0) * a.N + n;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+            pin(acc[i][j]);
+            if (m0 + i * 16 < t.mend && n + j * 16 < a.N)
+                *reinterpret_cast<v4f *>(out + (int64_t)(i * 16) * a.N + j * 16) = acc[i][j];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 template <class C, bool kGather>
 __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
 {
@@ -574,14 +610,14 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     Tiles<C::BM, C::BN, C::GROUP> tiles;
     tiles.init(a, lane);
-    const int count = tiles.count();
+    const int count = tiles.count(a);
     int v = blockIdx.x;
     if (v >= count)
         return;
     Tile t = tiles.find(a, v, lane);
     const int wm = wave / C::WN, wn = wave % C::WN;
     const int r = lane % 16, g = lane / 16;
-    const int numK = (int)((a.K + kB128 - 1) / kB128);
+    const int half = a.K % kB128 ? (int)(a.K / kB128) : -1;   // a last block of 64
 
     // Scales: chunk c of the tile into its buffer, 16 bytes of one row per lane
     // and, a dword per lane, those of the wavefront's columns.  Rows, and
@@ -600,11 +636,11 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
     auto load_scales = [&](int c) {
         char *sc = smem + C::kRing + (c & 1) * C::kScaleBytes;
         if (wave * 64 < C::BM)
-            gemm::lds_load16(rsx, (lds_void *)(sc + wave * 1024), soff, (uint32_t)c * C::kChunk);
+            gemm::lds_load16(rsx, (lds_void *)(sc + wave * 1024), soff,
+                             (uint32_t)(t.k0 + c * C::kChunk));
         lds_load4(rsw, (lds_void *)(sc + C::kScaleRows + wave * 256), lane % 4 * 4,
-                  (uint32_t)c * C::kChunk);
+                  (uint32_t)(t.k0 + c * C::kChunk));
     };
-    const int nchunk = (numK + C::kChunk - 1) / C::kChunk;
     unsigned sx[C::FM], sw;
     auto read_scales = [&](int kt) {
         const uint8_t *sc = reinterpret_cast<const uint8_t *>(smem) + C::kRing +
@@ -616,9 +652,8 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
     };
 
     Loader<C, kGather> ld;
-    const bool half = a.K % kB128 != 0;
     auto load_stage = [&](int s) {
-        const StageLoad<C, kGather> sl(ld, smem, s, numK, half);
+        const StageLoad<C, kGather> sl(ld, smem, t, s, half);
 #pragma unroll
         for (int j = 0; j < C::kLoads; ++j)
             sl.issue(ld, wave, j);
@@ -661,12 +696,12 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
             read_b(smem, j);
-        for (int kt = 0; kt < numK; ++kt) {
+        for (int kt = 0; kt < t.nk; ++kt) {
             const char *cbuf = smem + kt % C::STAGES * C::kStageBytes;
             const char *nbuf = smem + (kt + 1) % C::STAGES * C::kStageBytes;
-            const StageLoad<C, kGather> sl(ld, smem, kt + C::STAGES, numK, half);
+            const StageLoad<C, kGather> sl(ld, smem, t, kt + C::STAGES, half);
             // the other chunk's last bytes were read before the last barrier
-            if (kt % C::kChunk == 0 && kt / C::kChunk + 1 < nchunk)
+            if (kt % C::kChunk == 0 && kt + C::kChunk < t.nk)
                 load_scales(kt / C::kChunk + 1);
 #pragma unroll
             for (int m = 0; m < C::kMfmas; ++m) {
@@ -681,12 +716,12 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
                     __builtin_amdgcn_s_barrier();
                 }
                 if (m == C::kLand) {   // the next stage has landed for every wavefront
-                    wait_vm<(C::STAGES - 2) * C::kLoads + C::kBefore>();
+                    wait_vm<(C::STAGES - 2) * C::kLoads + C::before(C::kLand)>();
                     __builtin_amdgcn_s_barrier();
                 }
-                if (m >= C::kFree && (m - C::kFree) % C::kStep == 0 &&
-                    (m - C::kFree) / C::kStep < C::kLoads)
-                    sl.issue(ld, wave, (m - C::kFree) / C::kStep);
+#pragma unroll
+                for (int u = C::before(m); u < C::before(m + 1); ++u)
+                    sl.issue(ld, wave, u);
                 if (m >= C::kLand && (m - C::kLand) % 2 == 0 &&
                     (m - C::kLand) / 2 < 2 * (C::kPairs - 2))
                     read_a(nbuf, (m - C::kLand) / 2);
@@ -711,15 +746,43 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
             t = tiles.find(a, v, lane);
             start();
         }
-        if (a.type == kTypeBf16)
-            store_tile<C, kTypeBf16>(a, done, acc, smem + C::kRing + wave * C::kOutBytes, wm, wn,
+        if (a.parts)
+            store_parts<C>(a, done, acc, wm, wn, lane);
+        else if (a.type == kTypeBf16)
+            store_tile<C, kTypeBf16>(a, done, acc, smem + C::kOut + wave * C::kOutBytes, wm, wn,
                                      lane);
         else
-            store_tile<C, kTypeF16>(a, done, acc, smem + C::kRing + wave * C::kOutBytes, wm, wn,
+            store_tile<C, kTypeF16>(a, done, acc, smem + C::kOut + wave * C::kOutBytes, wm, wn,
                                     lane);
         if (v >= count)
             break;
     }
+}
+
+// out = act(sum of the parts + bias): 4 outputs per thread.
+template <int kT>
+__global__ __launch_bounds__(256) void k_b128_sum(B128Args a)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, size = a.M * a.N;
+    if (i >= size)
+        return;
+    v4f v = *reinterpret_cast<const v4f *>(a.parts + i);
+    for (int p = 1; p < a.nparts; ++p)
+        v += *reinterpret_cast<const v4f *>(a.parts + p * size + i);
+    uint2 b = make_uint2(0, 0);
+    if (a.bias)
+        b = *reinterpret_cast<const uint2 *>(a.bias + i % a.N);
+    *reinterpret_cast<uint2 *>(a.out + i) = finish4<kT>(v, b, lowest_output(a));
+}
+
+hipError_t launch_sum(const B128Args &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.M * a.N / 4 + 255) / 256));
+    if (a.type == kTypeBf16)
+        hipLaunchKernelGGL(k_b128_sum<kTypeBf16>, grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL(k_b128_sum<kTypeF16>, grid, dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 // The most tiles a launch may have: at most M / BM whole tile rows and a ragged
@@ -728,7 +791,8 @@ template <class C>
 int64_t most_tiles(const B128Args &a)
 {
     const int64_t ntn = (a.N + C::BN - 1) / C::BN;
-    return ntn * (a.offsets ? a.M / C::BM + (a.E < a.M ? a.E : a.M) : (a.M + C::BM - 1) / C::BM);
+    return ntn * a.nparts *
+           (a.offsets ? a.M / C::BM + (a.E < a.M ? a.E : a.M) : (a.M + C::BM - 1) / C::BM);
 }
 
 template <class C>

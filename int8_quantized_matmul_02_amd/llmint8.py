@@ -53,6 +53,9 @@ EXPORTS = (
     "llmint8_matmul_b128_workspace_bytes",
     "llmint8_matmul_b128",
     "llmint8_matmul_grouped_b128",
+    "llmint8_matmul_b128_workspace_bytes_path",
+    "llmint8_matmul_b128_path",
+    "llmint8_matmul_grouped_b128_path",
 )
 
 
@@ -112,11 +115,17 @@ def _load():
     lib.llmint8_quantize_weight_b128.argtypes = [P, I, I64, I64, I64, P, P, P]
     lib.llmint8_matmul_b128_workspace_bytes.argtypes = [I64, I64, I64]
     lib.llmint8_matmul_b128_workspace_bytes.restype = SZ
+    lib.llmint8_matmul_b128_workspace_bytes_path.argtypes = [I64, I64, I64, I, I]
+    lib.llmint8_matmul_b128_workspace_bytes_path.restype = SZ
     lib.llmint8_matmul_b128.argtypes = [P, P, I64, I64, I64, P, P, P, I, I, P, P, SZ, P]
+    lib.llmint8_matmul_b128_path.argtypes = [P, P, I64, I64, I64, P, P, P, I, I, P, P, SZ, I, I, P]
     lib.llmint8_matmul_grouped_b128.argtypes = [P, P, I64, I64, I64, P, P, I64, P, P, I64, P, I, I,
                                                 P, P]
+    lib.llmint8_matmul_grouped_b128_path.argtypes = [P, P, I64, I64, I64, P, P, I64, P, P, I64, P,
+                                                     I, I, P, I, P]
     for fn in ("llmint8_rmsnorm_b128", "llmint8_quantize_act_b128", "llmint8_quantize_weight_b128",
                "llmint8_matmul_b128", "llmint8_matmul_grouped_b128",
+               "llmint8_matmul_b128_path", "llmint8_matmul_grouped_b128_path",
                "llmint8_quantize_weight", "llmint8_quantize_act", "llmint8_matmul",
                "llmint8_matmul_act", "llmint8_matmul_path", "llmint8_igemm_i32",
                "llmint8_quantize_weight_zp", "llmint8_quantize_act_zp", "llmint8_matmul_zp",
@@ -578,11 +587,17 @@ def llmint8_matmul_e4m3(X, CB8, SC8, threshold=6.0, bias=None, out=None, ws=None
 # block of 128.  Codes are uint8 or torch.float8_e4m3fn, scales uint8 or
 # torch.float8_e8m0fnu (the same bytes); what is allocated here is uint8.
 # 16-bit tensors are float16 or bfloat16, all of one call of one dtype.
+#
+# A decoded token's calls take a few microseconds on the GPU, so the checks
+# here are one pass of attribute comparisons (_ok); only a call that fails one
+# goes through _arg and _on_device, for their message.
 # ---------------------------------------------------------------------------
 _TYPES = {torch.float16: 0, torch.bfloat16: 1}
 _T16 = (torch.float16, torch.bfloat16)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _SCALES = (torch.uint8, torch.float8_e8m0fnu)
+_U8 = torch.uint8
+_current_device = torch.cuda.current_device
 
 
 def llmint8_b128_pitch(K):
@@ -594,31 +609,36 @@ def _pitch(K):
     return (K + 511) // 512 * 4
 
 
-def _tensor(t, name, dtypes, ndim):
-    """An argument that sets a call's sizes: its type, dtype, dimensions and contiguity."""
-    _arg(t, name, dtypes)
-    if t.dim() != ndim:
-        raise ValueError("%s must be %d-D, got shape %s" % (name, ndim, tuple(t.shape)))
-    return t.shape
+def _sizes(t, name, dtypes, ndim):
+    """An argument that sets a call's sizes: its shape, and its device's index (-1: not a GPU)."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_contiguous():
+        _arg(t, name, dtypes)
+    shape = t.shape
+    if len(shape) != ndim:
+        raise ValueError("%s must be %d-D, got shape %s" % (name, ndim, tuple(shape)))
+    return shape
 
 
-class _on:
-    """The device of a call's tensors made current for its launch, and the
-    stream to use there (a stream handle belongs to its device)."""
+def _ok(dev, t, name, dtypes, shape):
+    """Whether argument `t` is on device `dev`; raises if it is of another
+    type, dtype or shape or not contiguous."""
+    if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape
+            or not t.is_contiguous()):
+        _arg(t, name, dtypes, shape=shape)
+    return t.get_device() == dev
 
-    def __init__(self, t):
-        self.dev = t.device
-        self.guard = None
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.dev.index:
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.dev).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _launch(fn, dev, *args):
+    """Calls the library with the stream of device `dev` as the last argument
+    (a stream handle belongs to its device, which has to be current)."""
+    f = getattr(_load(), fn)
+    if _current_device() == dev:
+        rc = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != LLMINT8_OK:
+        raise LLMInt8Error(fn, rc)
 
 
 def llmint8_rmsnorm_b128(X, gamma, eps=1e-6, residual=None, residual_out=None, Y=None, Xq8=None,
@@ -628,41 +648,55 @@ def llmint8_rmsnorm_b128(X, gamma, eps=1e-6, residual=None, residual_out=None, Y
     normalized rows and the sum X + residual, which is allocated if there is a residual
     and none is given (pass `residual` itself to update it in place).  Y: a tensor
     [T,K] that also receives the normalized rows in X's dtype."""
-    lib = _load()
-    T, K = _tensor(X, "X", _T16, 2)
-    dt = (X.dtype,)
-    d = X.device
-    _arg(gamma, "gamma", dt, shape=(K,))
+    shape = _sizes(X, "X", _T16, 2)
+    T, K = shape
+    d, dev, dt = X.device, X.get_device(), (X.dtype,)
+    ok = _ok(dev, gamma, "gamma", dt, (K,)) & (dev >= 0)
     if residual is not None:
-        _arg(residual, "residual", dt, shape=(T, K))
-        residual_out = _new_or(residual_out, "residual_out", dt, (T, K), d)
+        ok &= _ok(dev, residual, "residual", dt, shape)
+        if residual_out is not None:
+            ok &= _ok(dev, residual_out, "residual_out", dt, shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if Y is not None:
-        _arg(Y, "Y", dt, shape=(T, K))
-    Xq8 = _new_or(Xq8, "Xq8", _CODES, (T, K), d)
-    SX = _new_or(SX, "SX", _SCALES, (T, _pitch(K)), d)
-    _on_device(X=X, gamma=gamma, residual=residual, residual_out=residual_out, Y=Y, Xq8=Xq8, SX=SX)
-    with _on(X) as stream:
-        _check("llmint8_rmsnorm_b128",
-               lib.llmint8_rmsnorm_b128(X.data_ptr(), _ptr(residual), gamma.data_ptr(),
-                                        _TYPES[X.dtype], T, K, float(eps), Xq8.data_ptr(),
-                                        SX.data_ptr(), _ptr(residual_out), _ptr(Y), stream))
+        ok &= _ok(dev, Y, "Y", dt, shape)
+    if Xq8 is not None:
+        ok &= _ok(dev, Xq8, "Xq8", _CODES, shape)
+    if SX is not None:
+        ok &= _ok(dev, SX, "SX", _SCALES, (T, _pitch(K)))
+    if not ok:
+        _on_device(X=X, gamma=gamma, residual=residual, residual_out=residual_out, Y=Y, Xq8=Xq8,
+                   SX=SX)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(X)
+    if Xq8 is None:
+        Xq8 = torch.empty(shape, dtype=_U8, device=d)
+    if SX is None:
+        SX = torch.empty((T, _pitch(K)), dtype=_U8, device=d)
+    _launch("llmint8_rmsnorm_b128", dev, X.data_ptr(), _ptr(residual), gamma.data_ptr(),
+            _TYPES[X.dtype], T, K, eps, Xq8.data_ptr(), SX.data_ptr(), _ptr(residual_out), _ptr(Y))
     return Xq8, SX, residual_out
 
 
 def llmint8_quantize_act_b128(X, Xq8=None, SX=None):
     """X: fp16 or bf16 [T,K].  Returns (Xq8 uint8 [T,K] E4M3 codes, SX uint8 [T,pitch] scales of
     its 1 x 128 blocks)."""
-    lib = _load()
-    T, K = _tensor(X, "X", _T16, 2)
-    Xq8 = _new_or(Xq8, "Xq8", _CODES, (T, K), X.device)
-    SX = _new_or(SX, "SX", _SCALES, (T, _pitch(K)), X.device)
-    _on_device(X=X, Xq8=Xq8, SX=SX)
-    with _on(X) as stream:
-        _check("llmint8_quantize_act_b128",
-               lib.llmint8_quantize_act_b128(X.data_ptr(), _TYPES[X.dtype], T, K, Xq8.data_ptr(),
-                                             SX.data_ptr(), stream))
+    shape = _sizes(X, "X", _T16, 2)
+    T, K = shape
+    d, dev = X.device, X.get_device()
+    ok = dev >= 0
+    if Xq8 is not None:
+        ok &= _ok(dev, Xq8, "Xq8", _CODES, shape)
+    if SX is not None:
+        ok &= _ok(dev, SX, "SX", _SCALES, (T, _pitch(K)))
+    if not ok:
+        _on_device(X=X, Xq8=Xq8, SX=SX)
+    if Xq8 is None:
+        Xq8 = torch.empty(shape, dtype=_U8, device=d)
+    if SX is None:
+        SX = torch.empty((T, _pitch(K)), dtype=_U8, device=d)
+    _launch("llmint8_quantize_act_b128", dev, X.data_ptr(), _TYPES[X.dtype], T, K, Xq8.data_ptr(),
+            SX.data_ptr())
     return Xq8, SX
 
 
@@ -670,7 +704,6 @@ def llmint8_quantize_weight_b128(W_t, CB8=None, SB=None):
     """W_t: fp16 or bf16 [N,K], or [E,N,K] for the weights of E experts.  Returns (CB8 uint8 of
     the same shape, SB uint8 [ceil(N/128),pitch] or [E,ceil(N/128),pitch] scales of its
     128 x 128 blocks)."""
-    lib = _load()
     _arg(W_t, "W_t", _T16)
     if W_t.dim() not in (2, 3):
         raise ValueError("W_t must be [N,K] or [E,N,K], got shape %s" % (tuple(W_t.shape),))
@@ -680,36 +713,65 @@ def llmint8_quantize_weight_b128(W_t, CB8=None, SB=None):
     CB8 = _new_or(CB8, "CB8", _CODES, lead + (N, K), W_t.device)
     SB = _new_or(SB, "SB", _SCALES, lead + ((N + 127) // 128, _pitch(K)), W_t.device)
     _on_device(W_t=W_t, CB8=CB8, SB=SB)
-    with _on(W_t) as stream:
-        _check("llmint8_quantize_weight_b128",
-               lib.llmint8_quantize_weight_b128(W_t.data_ptr(), _TYPES[W_t.dtype], E, K, N,
-                                                CB8.data_ptr(), SB.data_ptr(), stream))
+    _launch("llmint8_quantize_weight_b128", W_t.get_device(), W_t.data_ptr(), _TYPES[W_t.dtype], E,
+            K, N, CB8.data_ptr(), SB.data_ptr())
     return CB8, SB
 
 
-def _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, M, lead):
-    """Checks the operands of a product ([E] = lead for the grouped one) and
-    returns its sizes and output; M None: as many rows as Xq8."""
-    T, K = _tensor(Xq8, "Xq8", _CODES, 2)
-    N = _tensor(CB8, "CB8", _CODES, 2 + len(lead))[-2]
-    if CB8.shape[-1] != K:
-        raise ValueError("shape mismatch: Xq8 %s, CB8 %s" % (tuple(Xq8.shape), tuple(CB8.shape)))
-    _arg(SX, "SX", _SCALES, shape=(T, _pitch(K)))
-    _arg(SB, "SB", _SCALES, shape=lead + ((N + 127) // 128, _pitch(K)))
+def _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, lead, offsets, row_idx, ws):
+    """Checks the operands of a product (lead = (E,) for the grouped one, with
+    offsets and row_idx) and returns its sizes T, K, N, M, its device and output."""
+    T, K = _sizes(Xq8, "Xq8", _CODES, 2)
+    wshape = _sizes(CB8, "CB8", _CODES, 2 + len(lead))
+    N = wshape[-2]
+    if wshape[-1] != K:
+        raise ValueError("shape mismatch: Xq8 %s, CB8 %s" % (tuple(Xq8.shape), tuple(wshape)))
+    dev = Xq8.get_device()
+    ok = (dev >= 0) & _ok(dev, SX, "SX", _SCALES, (T, _pitch(K)))
+    ok &= CB8.get_device() == dev
+    ok &= _ok(dev, SB, "SB", _SCALES, lead + ((N + 127) // 128, _pitch(K)))
+    M = T
+    if lead:
+        if row_idx is not None:
+            (M,) = _sizes(row_idx, "row_idx", (torch.int32,), 1)
+            ok &= row_idx.get_device() == dev
+        ok &= _ok(dev, offsets, "offsets", (torch.int32,), (lead[0] + 1,))
     if out is not None:
-        _arg(out, "out", _T16, shape=(T if M is None else M, N))
+        ok &= _ok(dev, out, "out", _T16, (M, N))
         out_dtype = out.dtype
     elif out_dtype not in _TYPES:
         raise TypeError("out_dtype must be float16 or bfloat16, got %s" % (out_dtype,))
     if bias is not None:
-        _arg(bias, "bias", (out_dtype,), shape=lead + (N,))
+        ok &= _ok(dev, bias, "bias", (out_dtype,), lead + (N,))
+    if ws is not None:
+        _arg(ws, "ws", (torch.uint8, torch.int8))
+        ok &= ws.get_device() == dev
+    if not ok:
+        _on_device(Xq8=Xq8, SX=SX, CB8=CB8, SB=SB, offsets=offsets, row_idx=row_idx, bias=bias,
+                   out=out, ws=ws)
     if out is None:
-        out = torch.empty((T if M is None else M, N), dtype=out_dtype, device=Xq8.device)
-    return T, K, N, out
+        out = torch.empty((M, N), dtype=out_dtype, device=Xq8.device)
+    return T, K, N, M, dev, out
 
 
-def llmint8_matmul_b128_workspace_bytes(T, K, N):
-    return int(_load().llmint8_matmul_b128_workspace_bytes(T, K, N))
+def llmint8_matmul_b128_workspace_bytes(T, K, N, path=0, parts=0):
+    return int(_load().llmint8_matmul_b128_workspace_bytes_path(T, K, N, path, parts))
+
+
+def llmint8_matmul_b128_path(Xq8, SX, CB8, SB, bias=None, activation=ACT_NONE, out=None,
+                             out_dtype=torch.float16, ws=None, path=0, parts=0):
+    """llmint8_matmul_b128 with the kernel's tile (path 1 .. 7) and the number of parts of K
+    chosen; 0 leaves the choice to the library."""
+    T, K, N, _, dev, out = _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, (), None, None,
+                                          ws)
+    if ws is None:
+        need = _load().llmint8_matmul_b128_workspace_bytes_path(T, K, N, path, parts)
+        if need:
+            ws = torch.empty((need,), dtype=_U8, device=Xq8.device)
+    _launch("llmint8_matmul_b128_path", dev, Xq8.data_ptr(), SX.data_ptr(), T, K, N,
+            CB8.data_ptr(), SB.data_ptr(), _ptr(bias), activation, _TYPES[out.dtype],
+            out.data_ptr(), _ptr(ws), 0 if ws is None else _nbytes(ws), path, parts)
+    return out
 
 
 def llmint8_matmul_b128(Xq8, SX, CB8, SB, bias=None, activation=ACT_NONE, out=None,
@@ -717,19 +779,26 @@ def llmint8_matmul_b128(Xq8, SX, CB8, SB, bias=None, activation=ACT_NONE, out=No
     """The product of block-scaled operands: codes Xq8 [T,K] and scales SX (from
     llmint8_quantize_act_b128 or llmint8_rmsnorm_b128), CB8 [N,K] and SB (from
     llmint8_quantize_weight_b128) -> out [T,N] in out_dtype (out's own dtype if given;
-    bias [N] has the same)."""
-    lib = _load()
-    T, K, N, out = _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, None, ())
-    need = lib.llmint8_matmul_b128_workspace_bytes(T, K, N)
-    if need or ws is not None:
-        ws = _ws(ws, need, Xq8.device)
-    _on_device(Xq8=Xq8, SX=SX, CB8=CB8, SB=SB, bias=bias, out=out, ws=ws)
-    with _on(Xq8) as stream:
-        _check("llmint8_matmul_b128",
-               lib.llmint8_matmul_b128(Xq8.data_ptr(), SX.data_ptr(), T, K, N, CB8.data_ptr(),
-                                       SB.data_ptr(), _ptr(bias), int(activation),
-                                       _TYPES[out.dtype], out.data_ptr(), _ptr(ws),
-                                       0 if ws is None else _nbytes(ws), stream))
+    bias [N] has the same).  ws: at least llmint8_matmul_b128_workspace_bytes(T, K, N)
+    bytes, allocated if needed and not given."""
+    return llmint8_matmul_b128_path(Xq8, SX, CB8, SB, bias, activation, out, out_dtype, ws)
+
+
+def llmint8_matmul_grouped_b128_path(Xq8, SX, CB8, SB, offsets, row_idx=None, bias=None,
+                                     activation=ACT_NONE, out=None, out_dtype=torch.float16,
+                                     path=0):
+    """llmint8_matmul_grouped_b128 with the kernel's tile chosen (path 1 .. 7; 0: the library's
+    choice)."""
+    if not isinstance(CB8, torch.Tensor) or CB8.dim() != 3:
+        raise ValueError("CB8 must be a tensor [E,N,K]")
+    E = CB8.shape[0]
+    T, K, N, M, dev, out = _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, (E,), offsets,
+                                          row_idx, None)
+    if M == 0:
+        return out
+    _launch("llmint8_matmul_grouped_b128_path", dev, Xq8.data_ptr(), SX.data_ptr(), T, K, N,
+            CB8.data_ptr(), SB.data_ptr(), E, offsets.data_ptr(), _ptr(row_idx), M, _ptr(bias),
+            activation, _TYPES[out.dtype], out.data_ptr(), path)
     return out
 
 
@@ -740,25 +809,5 @@ def llmint8_matmul_grouped_b128(Xq8, SX, CB8, SB, offsets, row_idx=None, bias=No
     device; row_idx int32 [M] on the device: output row i reads row row_idx[i] of Xq8 (row i
     without it).  Returns out [M,N]; rows outside [offsets[0], offsets[E]) are left as they were.
     M = 0 returns the empty output."""
-    lib = _load()
-    if not isinstance(CB8, torch.Tensor) or CB8.dim() != 3:
-        raise ValueError("CB8 must be a tensor [E,N,K]")
-    E = CB8.shape[0]
-    M = None
-    if row_idx is not None:
-        (M,) = _tensor(row_idx, "row_idx", (torch.int32,), 1)
-    T, K, N, out = _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, M, (E,))
-    M = T if M is None else M
-    _arg(offsets, "offsets", (torch.int32,), shape=(E + 1,))
-    _on_device(Xq8=Xq8, SX=SX, CB8=CB8, SB=SB, offsets=offsets, row_idx=row_idx, bias=bias,
-               out=out)
-    if M == 0:
-        return out
-    with _on(Xq8) as stream:
-        _check("llmint8_matmul_grouped_b128",
-               lib.llmint8_matmul_grouped_b128(Xq8.data_ptr(), SX.data_ptr(), T, K, N,
-                                               CB8.data_ptr(), SB.data_ptr(), E,
-                                               offsets.data_ptr(), _ptr(row_idx), M, _ptr(bias),
-                                               int(activation), _TYPES[out.dtype],
-                                               out.data_ptr(), stream))
-    return out
+    return llmint8_matmul_grouped_b128_path(Xq8, SX, CB8, SB, offsets, row_idx, bias, activation,
+                                            out, out_dtype)

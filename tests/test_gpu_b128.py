@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import int8_quantized_matmul_02_amd as L
+import int8_quantized_matmul_02_amd.llmint8  # noqa: F401  (L.llmint8: the kernel-forcing hooks)
 from tests import b128_ref as ref
 from tests.gpu_helpers import assert_equal_exact, dev, say
 
@@ -261,6 +262,51 @@ def test_matmul(K, N, exact):
         assert (out[T:] == 9.0).all(), "rows behind the output"
 
 
+@pytest.mark.parametrize("path", range(1, 8))
+@pytest.mark.parametrize("T,K,N", [(1, 64, 64), (70, 320, 192), (300, 1088, 576), (257, 2304, 320),
+                                   (530, 4160, 448)])
+def test_matmul_every_tile(T, K, N, path):
+    """Each tile shape at sizes that fill none of them, K whole and in parts,
+    the parts' sums between sentinels."""
+    for parts in (1, 2, 5, 8):
+        exact, dtype, relu = parts != 2, TYPES[parts % 2], parts == 5
+        say("matmul", T, K, N, "path", path, "parts", parts, dtype)
+        xq, sx, wq, sw = operands(T, K, N, T + K + N, exact=exact)
+        b = (rand((N,), dtype, N) * 4).round() / 4
+        need = L.llmint8.llmint8_matmul_b128_workspace_bytes(T, K, N, path, parts)
+        ws = torch.full((need + 256,), 0x5a, dtype=torch.uint8, device=dev())
+        out = torch.full((T + 1, N), 9.0, dtype=dtype, device=dev())
+        L.llmint8.llmint8_matmul_b128_path(*up(xq, sx, wq, sw), bias=b.to(dev()), out=out[:T],
+                                           activation=L.ACT_RELU if relu else L.ACT_NONE,
+                                           ws=ws[:need] if need else None, path=path, parts=parts)
+        v, S = expect(ref.values(xq, sx, 1), ref.values(wq, sw, 128), ref.to64(b), relu)
+        check_product(out[:T], v, S, K, dtype, exact, "path %d parts %d" % (path, parts))
+        assert (out[T:] == 9.0).all(), "rows behind the output"
+        assert (ws[need:] == 0x5a).all(), "behind the workspace"
+
+
+@pytest.mark.parametrize("path,T,K,N", [(7, 8100, 320, 4160), (6, 3000, 192, 5056),
+                                        (5, 4100, 576, 2112), (7, 4096, 1024, 4096)])
+def test_matmul_many_tiles(path, T, K, N):
+    """More tiles than a launch has blocks: each block takes several."""
+    say("many tiles", T, K, N, path)
+    d = dev()
+    X, W = hidden(T, K, torch.float16, 1).to(d), rand((N, K), torch.float16, 2, 0.02).to(d)
+    q, s = L.llmint8_quantize_act_b128(X)
+    c, sw = L.llmint8_quantize_weight_b128(W)
+    b = rand((N,), torch.bfloat16, 3).to(d)
+    got = L.llmint8.llmint8_matmul_b128_path(q, s, c, sw, bias=b, out_dtype=torch.bfloat16,
+                                             path=path, parts=1)
+    again = L.llmint8.llmint8_matmul_b128_path(q, s, c, sw, bias=b, out_dtype=torch.bfloat16,
+                                               path=path, parts=1)
+    assert torch.equal(got, again)
+    x = torch.from_numpy(ref.values(host(q), host(s), 1)).to(d)
+    w = torch.from_numpy(ref.values(host(c), host(sw), 128)).to(d)
+    v = x @ w.t().contiguous()
+    S = (x.abs() @ w.abs().t().contiguous() + b.double().abs()).cpu().numpy()
+    check_product(got, (v + b.double()).cpu().numpy(), S, K, torch.bfloat16, False, "many tiles")
+
+
 @pytest.mark.parametrize("T", [4, 60, 300])
 def test_matmul_range_of_scales(T):
     """Scales at both ends: products that overflow to infinity, vanish to
@@ -319,6 +365,52 @@ def test_grouped(K, N, exact):
                           ref.to64(b)[e] if bias else None, relu)
             check_product(out[lo:hi], v, S, K, dtype, exact, "%s expert %d" % (rows[:8], e))
         assert (out[:first] == 9.0).all() and (out[off[-1]:] == 9.0).all(), "rows of no group"
+
+
+@pytest.mark.parametrize("path", range(1, 8))
+def test_grouped_every_tile(path):
+    d = dev()
+    for rows, K, N, gather in (([70, 0, 129, 2], 320, 192, True), ([300, 5, 0, 31, 64], 192, 320, False),
+                               ([1] * 70 + [0] * 60 + [3], 576, 64, True),
+                               ([17, 600, 260], 1088, 576, True), ([513, 1, 255], 320, 320, False)):
+        E, M = len(rows), sum(rows) + 3
+        T = 45 if gather else M
+        say("grouped", rows[:5], E, K, N, "path", path)
+        xq, sx, wq, sw = operands(T, K, N, K + N, E=E, exact=True)
+        idx = np.random.default_rng(K).integers(0, T, M).astype(np.int32)
+        off = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+        out = torch.full((M, N), 9.0, dtype=torch.float16, device=d)
+        L.llmint8.llmint8_matmul_grouped_b128_path(
+            *up(xq, sx, wq, sw, off), row_idx=up(idx)[0] if gather else None, out=out, path=path)
+        x = ref.values(xq, sx, 1)
+        x = x[idx] if gather else x
+        for e in range(E):
+            lo, hi = off[e], off[e + 1]
+            v, S = expect(x[lo:hi], ref.values(wq[e], sw[e], 128), None, False)
+            check_product(out[lo:hi], v, S, K, torch.float16, True, "path %d expert %d" % (path, e))
+        assert (out[off[-1]:] == 9.0).all(), "rows of no group"
+
+
+@pytest.mark.parametrize("path", [5, 6, 7])
+def test_grouped_many_tiles(path):
+    """More tiles than a launch has blocks, of uneven groups."""
+    d, K, N, E = dev(), 320, 2112, 12
+    rows = [900, 1, 0, 2000, 64, 128, 0, 777, 257, 1500, 3, 640]
+    M, T = sum(rows), 500
+    say("grouped, many tiles", path, M)
+    X, W = hidden(T, K, torch.float16, 1).to(d), rand((E, N, K), torch.float16, 2, 0.02).to(d)
+    q, s = L.llmint8_quantize_act_b128(X)
+    c, sw = L.llmint8_quantize_weight_b128(W)
+    off = torch.tensor([0] + rows, device=d).cumsum(0).to(torch.int32)
+    idx = torch.randint(0, T, (M,), generator=torch.Generator().manual_seed(3)).to(torch.int32).to(d)
+    got = L.llmint8.llmint8_matmul_grouped_b128_path(q, s, c, sw, off, row_idx=idx, path=path)
+    x = torch.from_numpy(ref.values(host(q), host(s), 1)).to(d)[idx.long()]
+    b = host(off)
+    for e in range(E):
+        lo, hi = b[e], b[e + 1]
+        w = torch.from_numpy(ref.values(host(c[e]), host(sw[e]), 128)).to(d).t().contiguous()
+        v, S = (x[lo:hi] @ w).cpu().numpy(), (x[lo:hi].abs() @ w.abs()).cpu().numpy()
+        check_product(got[lo:hi], v, S, K, torch.float16, False, "expert %d" % e)
 
 
 def test_grouped_without_rows():
