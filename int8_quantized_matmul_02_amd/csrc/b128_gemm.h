@@ -252,41 +252,70 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
     const int64_t pitch = b128_pitch(a.K);
     const int nst = (t.nk + 3) / 4;   // stages of four blocks
 
-    // loads: instruction j of the block's fills staged rows 2j and 2j + 1 (the
-    // activations' first)
+    // Loads: instruction j of the block's fills staged rows 2j and 2j + 1 (the
+    // activations' first).  The weight's first stages are requested before
+    // anything that depends on row_idx, which is another trip to memory.
     const int64_t xr = x_base_row(a, t), wr = (int64_t)t.e * a.N + t.n0;
     const __amdgpu_buffer_rsrc_t rx = resource(a.Xq + xr * a.K, (a.rows - xr) * a.K);
     const __amdgpu_buffer_rsrc_t rw =
         resource(a.CB + wr * a.K, ((int64_t)a.E * a.N - wr) * a.K);
-    uint32_t off[C::kInstr];
-#pragma unroll
-    for (int u = 0; u < C::kInstr; ++u) {
-        const int r = 2 * (wave * C::kInstr + u) + lane / 32;
-        const int64_t row = r < C::BM ? source_row(a, t, t.m0 + r) - xr : r - C::BM;
-        off[u] = (uint32_t)(row * a.K + (((lane % 32) ^ (r & 15)) << 4));
-    }
-    // scales: slot s of the block's is row s's dword (s < BM), else the weight's
+    // the weight's scales are slots BM .. of the block's, the rows' before them
     const __amdgpu_buffer_rsrc_t rsx = resource(a.SX + xr * pitch, (a.rows - xr) * pitch);
     const __amdgpu_buffer_rsrc_t rsw = resource(
         a.SB + ((int64_t)t.e * scale_rows(a) + t.n0 / kB128) * pitch, pitch);
-    const int slot = wave * 64 + lane;
-    const bool xs = wave * 64 < C::BM;   // this wavefront fetches row scales
     static_assert(C::BM <= 64 || C::BM % 64 == 0, "row scales fill whole wavefronts");
-    const uint32_t soff =
-        xs ? (uint32_t)((source_row(a, t, t.m0 + (slot < C::BM ? slot : 0)) - xr) * pitch) : 0;
-
-    auto issue = [&](int s) {
-        char *st = smem + s % C::STAGES * C::kStageBytes;
-        const int sc = s < nst ? s : nst - 1;   // past the end: the last stage again, never read
-#pragma unroll
-        for (int u = 0; u < C::kInstr; ++u) {
-            const int j = wave * C::kInstr + u;
-            gemm::lds_load16(2 * j < C::BM ? rx : rw, (lds_void *)(st + j * 1024), off[u],
-                             (uint32_t)(t.k0 * kB128 + sc * C::kRowB));
-        }
-        lds_load4(xs ? rsx : rsw, (lds_void *)(st + (C::BM + C::BN) * C::kRowB + wave * 256), soff,
-                  (uint32_t)(t.k0 + sc * 4));
+    const bool xs = wave * 64 < C::BM;   // this wavefront fetches row scales
+    uint32_t off[C::kInstr], soff = 0;
+    auto staged_row = [&](int u) { return 2 * (wave * C::kInstr + u) + lane / 32; };
+    auto issue_one = [&](int s, int u) {
+        const int j = wave * C::kInstr + u;
+        gemm::lds_load16(2 * j < C::BM ? rx : rw,
+                         (lds_void *)(smem + s % C::STAGES * C::kStageBytes + j * 1024), off[u],
+                         (uint32_t)(t.k0 * kB128 + (s < nst ? s : nst - 1) * C::kRowB));
     };
+    auto issue_scales = [&](int s) {
+        lds_load4(xs ? rsx : rsw,
+                  (lds_void *)(smem + s % C::STAGES * C::kStageBytes +
+                               (C::BM + C::BN) * C::kRowB + wave * 256),
+                  soff, (uint32_t)(t.k0 + (s < nst ? s : nst - 1) * 4));
+    };
+    // stage s (past the end: the last stage again, never read)
+    auto issue = [&](int s) {
+#pragma unroll
+        for (int u = 0; u < C::kInstr; ++u)
+            issue_one(s, u);
+        issue_scales(s);
+    };
+#pragma unroll
+    for (int u = 0; u < C::kInstr; ++u) {
+        const int r = staged_row(u);
+        off[u] = (uint32_t)((r - C::BM) * a.K + (((lane % 32) ^ (r & 15)) << 4));
+    }
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s)
+#pragma unroll
+        for (int u = 0; u < C::kInstr; ++u)
+            if (2 * (wave * C::kInstr + u) >= C::BM)
+                issue_one(s, u);
+#pragma unroll
+    for (int u = 0; u < C::kInstr; ++u) {
+        const int r = staged_row(u);
+        if (2 * (wave * C::kInstr + u) < C::BM)
+            // rows behind the group's: zeros, without a memory access
+            off[u] = t.m0 + r < t.mend ? (uint32_t)((source_row(a, t, t.m0 + r) - xr) * a.K +
+                                                    (((lane % 32) ^ (r & 15)) << 4))
+                                       : kNowhere;
+    }
+    if (xs)
+        soff = (uint32_t)((source_row(a, t, t.m0 + (tid < C::BM ? tid : 0)) - xr) * pitch);
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s) {
+#pragma unroll
+        for (int u = 0; u < C::kInstr; ++u)
+            if (2 * (wave * C::kInstr + u) < C::BM)
+                issue_one(s, u);
+        issue_scales(s);
+    }
 
     v4f acc[C::FM][C::FN];
 #pragma unroll
@@ -304,13 +333,13 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
         return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     };
 
-#pragma unroll
-    for (int s = 0; s < C::STAGES - 1; ++s)
-        issue(s);
     for (int kt = 0; kt < nst; ++kt) {
         // stage kt has landed for this wavefront, then for all; they are also
         // done reading stage kt - 1, whose buffer stage kt + STAGES - 1 takes
-        wait_vm<(C::STAGES - 2) * C::kLoads>();
+        if (kt == 0)
+            wait_vm<0>();   // the first stages' loads were not issued stage by stage
+        else
+            wait_vm<(C::STAGES - 2) * C::kLoads>();
         __builtin_amdgcn_s_barrier();
         issue(kt + C::STAGES - 1);
         const char *st = smem + kt % C::STAGES * C::kStageBytes;
