@@ -4,44 +4,62 @@
 
 namespace llmint8 {
 
-using Small16 = b128::SmallCfg<16, 16, 1, 1, 4, 4>;
-using Small16x32 = b128::SmallCfg<16, 32, 1, 1, 4, 3>;
-using Small32 = b128::SmallCfg<32, 32, 1, 1, 4, 2>;
-using Small64 = b128::SmallCfg<64, 64, 2, 2, 1, 2>;
-using Big64 = b128::BigCfg<64, 128, 1, 4, 3, 4>;
+// Few rows: 4 or 8 wavefronts per block, K split over 4 of them (64 x 64: over
+// 2); many rows: 4 wavefronts.
+using Small16x16 = b128::SmallCfg<16, 16, 1, 1, 4, 4>;
+using Small16x32 = b128::SmallCfg<16, 32, 1, 2, 4, 3>;
+using Small16x32s2 = b128::SmallCfg<16, 32, 1, 2, 4, 2>;
+using Small16x64 = b128::SmallCfg<16, 64, 1, 2, 4, 3>;
+using Small32x64 = b128::SmallCfg<32, 64, 1, 2, 4, 3>;
+using Small64x64 = b128::SmallCfg<64, 64, 2, 2, 2, 2>;
+using Big64x128 = b128::BigCfg<64, 128, 1, 4, 3, 4>;
 using Big128 = b128::BigCfg<128, 128, 2, 2, 2, 4>;
 using Big256 = b128::BigCfg<256, 256, 2, 2, 2, 4>;
 
 namespace {
 
-// The tile and the parts of K, by an estimate in microseconds that follows
-// what the sweeps on MI355X showed.  A block reads (BM + BN) * K bytes, at 52
-// KB/us per compute unit whatever its shape (the 13 TB/s that all of them
-// draw from L2 together); only 256 x 256 reaches the matrix cores' pace, 1.5
-// us per block of K.  The weight comes from HBM once at 5 TB/s.  A block costs
-// `fixed` besides (first loads, output), less where several are resident; a
-// split of K costs a second launch and its partial sums, written and read.
-// Measured (us; the estimate's choice first): 300 x 2048 x 8192 128 x 128 12.8,
-// 64 x 128 15.4, 64 x 64 24.7; 256 x 4096 x 4096 64 x 64 14.8, 64 x 128 17.1, 128 x 128
-// 20.3; 64 x 16384 x 4096 64 x 128 in 8 parts 20.9, 128 x 128 in 8 23.4, 32 x 32 whole
-// 32.1; 512 x 16384 x 4096 128 x 128 in 4 parts 51.2, 64 x 128 whole 57.0; 1 x 4096
-// x 4096 16 x 16 5.9, 16 x 32 6.5; 64 experts with one row, K = 2048, N = 1024: 16 x 32
-// 34.7, 16 x 16 44.6.
+// The tile and the parts of K are those with the least estimated time.  In
+// microseconds, with what sweeps over 139 sizes on MI355X showed:
+//   * a block reads (BM + BN) * K bytes at what its compute unit draws: the
+//     bytes its resident blocks keep in flight over 0.9 us of latency, at most
+//     57 KB/us (all units together 14.6 TB/s, from L2);
+//   * 256 x 256 is bound by the matrix cores instead, 1.5 us per block of K;
+//   * a block costs `fixed` besides, shared by those resident together;
+//   * the weight comes from HBM at 5 TB/s; the longer of reading it and of the
+//     blocks counts whole, the shorter for three quarters (they overlap in part);
+//   * a split of K adds a launch and its partial sums, written and read.
+// Over the sweep the choice took 2.7 % longer than the best of 16 shapes with
+// 1, 2, 4 or 8 parts (geometric mean; these nine shapes at best 0.5 %).  Some
+// of it, in us: 1 x 4096 x 16384 16 x 64 16.2, 16 x 16 17.6; 1 x 16384 x 4096 16 x 16 15.0,
+// 16 x 64 23.7; 64 experts with a row or two, K = 2048, N = 1024: 16 x 32 20.4, 16 x 16
+// 31.3; 300 x 2048 x 8192: 128 x 128 12.8, 64 x 128 15.4; 256 x 16384 x 4096: 128 x 128 in
+// 4 parts 36, whole 90; 4096 x 4096 x 16384: 256 x 256 208, 128 x 128 349.
 struct Shape {
     int bm, bn;
-    double fixed, per_block;   // per_block: us per block of K if not bound by reading
+    int resident;         // blocks per compute unit
+    double in_flight;     // bytes a block keeps on their way
+    double fixed, pace;   // pace: us per block of K at the least
     hipError_t (*launch)(const B128Args &, hipStream_t);
 };
+template <class C>
+constexpr Shape small_shape()
+{
+    return {C::BM, C::BN, 160 * 1024 / C::kLdsBytes, (C::STAGES - 1.0) * (C::BM + C::BN) * C::kRowB,
+            1.0, 0.0, b128::launch_small<C>};
+}
+template <class C>
+constexpr Shape big_shape(double fixed, double pace)
+{
+    // the buffer of the stage being multiplied is refilled early on
+    return {C::BM, C::BN, C::kPerCu, (C::STAGES - 0.3) * C::kStageBytes, fixed, pace,
+            b128::launch_big<C>};
+}
 const Shape kShapes[kB128Paths] = {
-    {16, 16, 0.8, 0.0, b128::launch_small<Small16>},
-    {16, 32, 0.8, 0.0, b128::launch_small<Small16x32>},
-    {32, 32, 0.8, 0.0, b128::launch_small<Small32>},
-    {64, 64, 1.5, 0.0, b128::launch_small<Small64>},
-    {64, 128, 1.0, 0.0, b128::launch_big<Big64>},
-    {128, 128, 1.0, 0.0, b128::launch_big<Big128>},
-    {256, 256, 4.0, 1.5, b128::launch_big<Big256>},
+    small_shape<Small16x16>(),   small_shape<Small16x32>(), small_shape<Small16x32s2>(),
+    small_shape<Small16x64>(),   small_shape<Small32x64>(), small_shape<Small64x64>(),
+    big_shape<Big64x128>(1.0, 0.0), big_shape<Big128>(1.0, 0.0), big_shape<Big256>(5.0, 1.5),
 };
-constexpr double kCuRate = 52e3, kHbmRate = 5e6;   // bytes per us
+constexpr double kLatency = 0.9, kCuRate = 57e3, kHbmRate = 5e6, kSumRate = 8e6;   // us, bytes per us
 constexpr int kCUs = 256;
 constexpr int64_t kMostParts = (int64_t)128 << 20;   // bytes of partial sums
 
@@ -55,7 +73,7 @@ struct Plan {
 Plan choose(int64_t M, int64_t K, int64_t N, int64_t E, bool grouped, int path, int only)
 {
     const int64_t nblk = (K + kB128 - 1) / kB128, used = E < M ? E : M;
-    const double hbm = (double)used * N * K / kHbmRate;
+    const double hbm = (double)(grouped ? used : 1) * N * K / kHbmRate;
     Plan best{&kShapes[0], 1, (int)nblk};
     double least = 1e300;
     for (int i = 0; i < kB128Paths; ++i) {
@@ -69,19 +87,24 @@ Plan choose(int64_t M, int64_t K, int64_t N, int64_t E, bool grouped, int path, 
             ntm = ntm < used ? used : ntm;
         }
         const double tiles = ntm * ((N + s.bn - 1) / s.bn);
-        for (int parts = only ? only : 1; parts <= 8; parts *= 2) {
+        double rows = M / ntm;   // of a tile; those without an output are not read
+        rows = rows < 1 ? 1 : rows < s.bm ? rows : s.bm;
+        for (int parts = only ? only : 1; parts <= kB128MostParts; parts *= 2) {
             if (parts > 1 && !only &&
                 (grouped || nblk < 8 * parts || parts * M * N * 4 > kMostParts))
                 break;
             const int per = (int)((nblk + parts - 1) / parts + 3) / 4 * 4;   // whole dwords of scales
             const int n = (int)((nblk + per - 1) / per);
-            const double read = (double)(s.bm + s.bn) * per * kB128 / kCuRate;
-            const double one = s.fixed + (read > per * s.per_block ? read : per * s.per_block);
-            const double rounds = __builtin_ceil(tiles * n / kCUs);
-            double t = rounds * one;
-            t = t < hbm ? hbm : t;
+            const double per_cu = __builtin_ceil(tiles * n / kCUs);
+            const double here = per_cu < s.resident ? per_cu : s.resident;
+            double rate = here * s.in_flight / kLatency;
+            rate = rate < kCuRate ? rate : kCuRate;
+            double one = (rows + s.bn) * per * kB128 / rate;
+            one = (one < per * s.pace ? per * s.pace : one) + s.fixed / here;
+            const double blocks = per_cu * one;
+            double t = blocks < hbm ? hbm + 0.75 * blocks : blocks + 0.75 * hbm;
             if (n > 1)
-                t += 3.0 + 2.0 * n * M * N * 4 / kHbmRate;
+                t += 3.0 + 2.0 * n * M * N * 4 / kSumRate;
             if (t < least) {
                 least = t;
                 best = Plan{&s, n, per};

@@ -262,7 +262,7 @@ def test_matmul(K, N, exact):
         assert (out[T:] == 9.0).all(), "rows behind the output"
 
 
-@pytest.mark.parametrize("path", range(1, 8))
+@pytest.mark.parametrize("path", range(1, 10))
 @pytest.mark.parametrize("T,K,N", [(1, 64, 64), (70, 320, 192), (300, 1088, 576), (257, 2304, 320),
                                    (530, 4160, 448)])
 def test_matmul_every_tile(T, K, N, path):
@@ -285,8 +285,8 @@ def test_matmul_every_tile(T, K, N, path):
         assert (ws[need:] == 0x5a).all(), "behind the workspace"
 
 
-@pytest.mark.parametrize("path,T,K,N", [(7, 8100, 320, 4160), (6, 3000, 192, 5056),
-                                        (5, 4100, 576, 2112), (7, 4096, 1024, 4096)])
+@pytest.mark.parametrize("path,T,K,N", [(9, 8100, 320, 4160), (8, 3000, 192, 5056),
+                                        (7, 4100, 576, 2112), (9, 4096, 1024, 4096)])
 def test_matmul_many_tiles(path, T, K, N):
     """More tiles than a launch has blocks: each block takes several."""
     say("many tiles", T, K, N, path)
@@ -367,7 +367,7 @@ def test_grouped(K, N, exact):
         assert (out[:first] == 9.0).all() and (out[off[-1]:] == 9.0).all(), "rows of no group"
 
 
-@pytest.mark.parametrize("path", range(1, 8))
+@pytest.mark.parametrize("path", range(1, 10))
 def test_grouped_every_tile(path):
     d = dev()
     for rows, K, N, gather in (([70, 0, 129, 2], 320, 192, True), ([300, 5, 0, 31, 64], 192, 320, False),
@@ -391,7 +391,7 @@ def test_grouped_every_tile(path):
         assert (out[off[-1]:] == 9.0).all(), "rows of no group"
 
 
-@pytest.mark.parametrize("path", [5, 6, 7])
+@pytest.mark.parametrize("path", [7, 8, 9])
 def test_grouped_many_tiles(path):
     """More tiles than a launch has blocks, of uneven groups."""
     d, K, N, E = dev(), 320, 2112, 12
