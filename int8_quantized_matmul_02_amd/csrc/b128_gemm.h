@@ -178,21 +178,24 @@ __device__ __forceinline__ unsigned buf_load4(__amdgpu_buffer_rsrc_t r, uint32_t
     return __builtin_amdgcn_raw_buffer_load_b32(r, voffset, soffset, 0);
 }
 
-// Four finished outputs of consecutive columns: bias (0 without one),
-// activation (lowest: 0, or -infinity without one; a NaN stays), rounding.
-// No branches, so that the callers' unrolled loops stay straight.
+// Four finished outputs of consecutive columns: activation (lowest: 0, or
+// -infinity without one; a NaN stays) and rounding.  No branches, so that the
+// callers' unrolled loops stay straight.
 template <int kT>
-__device__ __forceinline__ uint2 finish4(v4f v, uint2 b, float lowest)
+__device__ __forceinline__ uint2 finish4(v4f v, float lowest)
 {
-    v[0] += t2f<kT>((uint16_t)b.x);
-    v[1] += t2f<kT>((uint16_t)(b.x >> 16));
-    v[2] += t2f<kT>((uint16_t)b.y);
-    v[3] += t2f<kT>((uint16_t)(b.y >> 16));
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-        v[q] = v[q] < lowest ? lowest : v[q];
+        v[q] = __builtin_elementwise_maximum(v[q], lowest);
     return make_uint2(f2t<kT>(v[0]) | (unsigned)f2t<kT>(v[1]) << 16,
                       f2t<kT>(v[2]) | (unsigned)f2t<kT>(v[3]) << 16);
+}
+// Four bias values (zeros without a bias).
+template <int kT>
+__device__ __forceinline__ v4f bias4(uint2 b)
+{
+    return v4f{t2f<kT>((uint16_t)b.x), t2f<kT>((uint16_t)(b.x >> 16)), t2f<kT>((uint16_t)b.y),
+               t2f<kT>((uint16_t)(b.y >> 16))};
 }
 __device__ __forceinline__ float lowest_output(const B128Args &a)
 {
@@ -404,7 +407,8 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
         if (a.bias)
             b = *reinterpret_cast<const uint2 *>(a.bias + (int64_t)t.e * a.N + n);
         uint2 *o = reinterpret_cast<uint2 *>(a.out + (int64_t)(t.m0 + row) * a.N + n);
-        *o = a.type == kTypeBf16 ? finish4<kTypeBf16>(v, b, lowest) : finish4<kTypeF16>(v, b, lowest);
+        *o = a.type == kTypeBf16 ? finish4<kTypeBf16>(v + bias4<kTypeBf16>(b), lowest)
+                                 : finish4<kTypeF16>(v + bias4<kTypeF16>(b), lowest);
     }
 }
 
@@ -457,6 +461,8 @@ struct BigCfg {
     static constexpr int kStageBytes = (BM + BN) * 128;
     static constexpr int kRing = STAGES * kStageBytes;
     static constexpr int kOutBytes = 16 * kTN * 2;             // a wavefront's output staging
+    static constexpr int kPieces = kTN / 8, kRowsPerStore = 64 / kPieces;   // 16 bytes per lane
+    static constexpr int kStores = FM * 16 / kRowsPerStore;    // store instructions per tile
     static constexpr int kChunk = 16;                          // stages per chunk of scales
     static constexpr int kScaleRows = BM * kChunk;             // then 256 bytes per wavefront: its columns'
     static constexpr int kScaleBytes = kScaleRows + kWaves * 256;
@@ -485,6 +491,7 @@ struct BigCfg {
     static_assert(kTN <= kB128 && kB128 % kTN == 0, "a wavefront's columns share a scale row");
     static_assert(FM >= 4 && FM % 2 == 0, "pairs");
     static_assert(STAGES >= 2 && (STAGES - 1) * kLoads < 64, "vmcnt range");
+    static_assert((STAGES - 1) * kLoads + kStores < 64, "vmcnt range");
     static_assert(kPerCu >= 1, "LDS");
     static_assert(BM % 64 == 0 && BM <= 64 * kWaves, "scales: a row per lane");
 };
@@ -565,46 +572,54 @@ __device__ __forceinline__ v8i read_frag(const char *p0, const char *p1)
     const v4i lo = *reinterpret_cast<const v4i *>(p0), hi = *reinterpret_cast<const v4i *>(p1);
     return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
+__device__ __forceinline__ void buf_store16(uint4 v, __amdgpu_buffer_rsrc_t r, uint32_t voffset)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(v4i{(int)v.x, (int)v.y, (int)v.z, (int)v.w}, r, voffset, 0,
+                                           0);
+}
+
 // A finished wavefront tile, out through the wavefront's own staging `st`, 16
 // rows of its kTN columns at a time, so that a store instruction fills whole
 // lines.  A lane holds 4 columns (unit u = 4j + g) of row r; the unit sits in
-// slot u ^ 2r, so that the rows write without conflicts.
+// slot u ^ 2r, so that the rows write without conflicts.  The stores go
+// through buffer resources that end with the group's last row, so that every
+// tile issues C::kStores of them.
 template <class C, int kT>
 __device__ __forceinline__ void store_tile(const B128Args &a, const Tile &t,
                                            v4f (&acc)[C::FM][C::FN], char *st, int wm, int wn,
                                            int lane)
 {
-    constexpr int kUnits = C::kTN / 4, kMask = kUnits - 1;
-    constexpr int kPieces = C::kTN / 8, kRowsPerStore = 64 / kPieces;
-    const int r = lane % 16, g = lane / 16, pc = lane % kPieces, pr = lane / kPieces;
-    const int64_t nw = t.n0 + wn * C::kTN, n = nw + 8 * pc;
-    const int m0 = t.m0 + wm * C::kTM + pr;
-    uint2 bias[C::FN];
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
-        bias[j] = make_uint2(0, 0);
-        if (a.bias)
-            bias[j] = *reinterpret_cast<const uint2 *>(
-                a.bias + (int64_t)t.e * a.N + min(nw + j * 16 + 4 * g, a.N - 4));
-    }
-    uint16_t *out = a.out + (int64_t)m0 * a.N + n;
+    constexpr int kMask = C::kTN / 4 - 1;
+    const int r = lane % 16, g = lane / 16, pc = lane % C::kPieces, pr = lane / C::kPieces;
+    const int64_t nw = t.n0 + wn * C::kTN;
     const float lowest = lowest_output(a);
+    char *put[C::FN];
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+        put[j] = st + r * (C::kTN * 2) + 8 * ((4 * j + g) ^ (2 * r & kMask));
+    uint32_t off[16 / C::kRowsPerStore];
+#pragma unroll
+    for (int q = 0; q < 16 / C::kRowsPerStore; ++q)
+        off[q] = nw + 8 * pc < a.N ? (uint32_t)((q * C::kRowsPerStore + pr) * a.N * 2 + 16 * pc)
+                                   : kNowhere;
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
             pin(acc[i][j]);   // stays an accumulator register until its turn
-            *reinterpret_cast<uint2 *>(st + r * (C::kTN * 2) + 8 * ((4 * j + g) ^ (2 * r & kMask))) =
-                finish4<kT>(acc[i][j], bias[j], lowest);
+            *reinterpret_cast<uint2 *>(put[j]) = finish4<kT>(acc[i][j], lowest);
         }
         __builtin_amdgcn_wave_barrier();
+        const int64_t row = t.m0 + wm * C::kTM + i * 16, left = t.mend - row;
+        const __amdgpu_buffer_rsrc_t out = resource(
+            reinterpret_cast<const uint8_t *>(a.out + row * a.N + nw),
+            left > 0 && nw < a.N ? (left * a.N - nw) * 2 : 0);
 #pragma unroll
-        for (int q = 0; q < 16; q += kRowsPerStore) {
-            const int row = q + pr;
-            const uint4 w = *reinterpret_cast<const uint4 *>(
-                st + row * (C::kTN * 2) + 16 * (pc ^ (row & (kMask >> 1))));
-            if (m0 + i * 16 + q < t.mend && n < a.N)
-                *reinterpret_cast<uint4 *>(out + (int64_t)(i * 16 + q) * a.N) = w;
+        for (int q = 0; q < 16 / C::kRowsPerStore; ++q) {
+            const int x = q * C::kRowsPerStore + pr;
+            buf_store16(*reinterpret_cast<const uint4 *>(st + x * (C::kTN * 2) +
+                                                         16 * (pc ^ (x & (kMask >> 1)))),
+                        out, off[q]);
         }
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_sched_barrier(0);
@@ -670,9 +685,9 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
         lds_load4(rsw, (lds_void *)(sc + C::kScaleRows + wave * 256), lane % 4 * 4,
                   (uint32_t)(t.k0 + c * C::kChunk));
     };
-    unsigned sx[C::FM], sw;
+    int sx[C::FM], sw;   // the MFMA reads the low byte
     auto read_scales = [&](int kt) {
-        const uint8_t *sc = reinterpret_cast<const uint8_t *>(smem) + C::kRing +
+        const int8_t *sc = reinterpret_cast<const int8_t *>(smem) + C::kRing +
                             (kt / C::kChunk & 1) * C::kScaleBytes + kt % C::kChunk;
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
@@ -687,8 +702,17 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
         for (int j = 0; j < C::kLoads; ++j)
             sl.issue(ld, wave, j);
     };
-    // a tile's first scales and stages
+    // a tile's bias (its products are summed onto it), first scales and stages
+    uint2 bias[C::FN];
     auto start = [&]() {
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+            bias[j] = make_uint2(0, 0);
+            if (a.bias && !a.parts)
+                bias[j] = *reinterpret_cast<const uint2 *>(
+                    a.bias + (int64_t)t.e * a.N +
+                    min(t.n0 + wn * C::kTN + j * 16 + 4 * g, a.N - 4));
+        }
         scale_rows_of(t);
         load_scales(0);
         ld.init(a, t, wave, lane);
@@ -709,14 +733,20 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
         fb[j] = read_frag(buf + boff + j * 2048 + fo0, buf + boff + j * 2048 + fo1);
     };
 
-    for (;;) {
+    for (bool first = true;; first = false) {
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
+        for (int j = 0; j < C::FN; ++j) {
+            const v4f b = a.type == kTypeBf16 ? bias4<kTypeBf16>(bias[j]) : bias4<kTypeF16>(bias[j]);
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j)
-                acc[i][j] = v4f{0, 0, 0, 0};
-        // the first stage and scales have landed; its fragments, but for A's last pair
-        wait_vm<(C::STAGES - 1) * C::kLoads>();
+            for (int i = 0; i < C::FM; ++i)
+                acc[i][j] = b;
+        }
+        // The first stage and scales have landed; its fragments, but for A's
+        // last pair.  The stores of the tile before are younger and may go on.
+        if (first || a.parts)
+            wait_vm<(C::STAGES - 1) * C::kLoads>();
+        else
+            wait_vm<(C::STAGES - 1) * C::kLoads + C::kStores>();
         __builtin_amdgcn_s_barrier();
         read_scales(0);
 #pragma unroll
@@ -801,7 +831,7 @@ __global__ __launch_bounds__(256) void k_b128_sum(B128Args a)
     uint2 b = make_uint2(0, 0);
     if (a.bias)
         b = *reinterpret_cast<const uint2 *>(a.bias + i % a.N);
-    *reinterpret_cast<uint2 *>(a.out + i) = finish4<kT>(v, b, lowest_output(a));
+    *reinterpret_cast<uint2 *>(a.out + i) = finish4<kT>(v + bias4<kT>(b), lowest_output(a));
 }
 
 hipError_t launch_sum(const B128Args &a, hipStream_t s)
