@@ -90,8 +90,10 @@ Plan choose(int64_t M, int64_t K, int64_t N, int64_t E, bool grouped, int path, 
         double rows = M / ntm;   // of a tile; those without an output are not read
         rows = rows < 1 ? 1 : rows < s.bm ? rows : s.bm;
         for (int parts = only ? only : 1; parts <= kB128MostParts; parts *= 2) {
+            // parts only while half as many leave compute units without their blocks
             if (parts > 1 && !only &&
-                (grouped || nblk < 8 * parts || parts * M * N * 4 > kMostParts))
+                (grouped || nblk < 8 * parts || parts * M * N * 4 > kMostParts ||
+                 tiles * (parts / 2) >= kCUs * s.resident))
                 break;
             const int per = (int)((nblk + parts - 1) / parts + 3) / 4 * 4;   // whole dwords of scales
             const int n = (int)((nblk + per - 1) / per);

@@ -84,8 +84,11 @@ __device__ __forceinline__ uint2 quant8_b128(uint4 v, float mul)
 // it exactly), NC chunks of 8 elements each; chunk c belongs to thread
 // c % TPR, so 16 consecutive lanes hold one block of 128 and find its largest
 // magnitude by lane exchanges.  One pass over memory: sums of squares, the
-// normalized values and their codes all come from the registers.
+// normalized values and their codes all come from the registers.  Loads go out
+// kBatch chunks of X and the residual at a time.
 // ---------------------------------------------------------------------------
+constexpr int kBatch = 4;
+
 template <int kT, int TPR, int NC>
 __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void k_rmsnorm_b128(RmsNormArgs a,
                                                                                 int pitch)
@@ -100,35 +103,38 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void k_rmsnorm_b12
     const uint4 *r = reinterpret_cast<const uint4 *>(a.R ? a.R + row * a.K : a.X);
     const uint4 *g = reinterpret_cast<const uint4 *>(a.G);
 
-    uint4 h[NC], gm[NC];
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
+    uint4 h[NC], gm[NC < kBatch ? NC : kBatch];
+    // Chunk j, or zeros past the row's end.
+    auto load = [&](const uint4 *p, int j) {
         const int c = tid + j * TPR;
-        h[j] = c < nchunk ? x[c] : make_uint4(0, 0, 0, 0);
-    }
-    if (a.R) {
-        uint4 rr[NC];
+        return c < nchunk ? p[c] : make_uint4(0, 0, 0, 0);
+    };
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            const int c = tid + j * TPR;
-            rr[j] = c < nchunk ? r[c] : make_uint4(0, 0, 0, 0);
+    for (int j0 = 0; j0 < NC; j0 += kBatch) {
+        uint4 rr[kBatch];
+#pragma unroll
+        for (int j = j0; j < NC && j < j0 + kBatch; ++j)
+            h[j] = load(x, j);
+        if (a.R) {
+#pragma unroll
+            for (int j = j0; j < NC && j < j0 + kBatch; ++j)
+                rr[j - j0] = load(r, j);
+#pragma unroll
+            for (int j = j0; j < NC && j < j0 + kBatch; ++j) {
+                float p[8], q[8];
+                unpack8<kT>(h[j], p);
+                unpack8<kT>(rr[j - j0], q);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    p[i] += q[i];
+                h[j] = pack8<kT>(p);
+            }
         }
-#pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            float p[8], q[8];
-            unpack8<kT>(h[j], p);
-            unpack8<kT>(rr[j], q);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                p[i] += q[i];
-            h[j] = pack8<kT>(p);
-        }
     }
+    // the first chunks' gamma comes under the reduction
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        const int c = tid + j * TPR;
-        gm[j] = c < nchunk ? g[c] : make_uint4(0, 0, 0, 0);
-    }
+    for (int j = 0; j < NC && j < kBatch; ++j)
+        gm[j] = load(g, j);
     float ss = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
@@ -165,7 +171,7 @@ __global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void k_rmsnorm_b12
         const bool in = c < nchunk;
         float y[8], gg[8];
         unpack8<kT>(h[j], y);
-        unpack8<kT>(gm[j], gg);
+        unpack8<kT>(j < kBatch ? gm[j < kBatch ? j : 0] : load(g, j), gg);
         unsigned m = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -313,11 +319,30 @@ __global__ __launch_bounds__(kThreads) void k_quantize_weight_b128(
 
 hipError_t launch_rmsnorm_b128(const RmsNormArgs &a, int type, hipStream_t s)
 {
-    const int64_t n = a.K / 8;   // chunks per row
-    if (n <= 256 * 2)
-        return launch_norm<256, 2>(a, type, s);
-    if (n <= 256 * 8)
-        return launch_norm<256, 8>(a, type, s);
+    // Threads per row and chunks per thread: as few chunks as hold the row, as
+    // many threads as leave none idle.  Measured on MI355X with a residual (us,
+    // against the next best or a wider row's form): 8192 x 256 6.7 (7.9), 8192 x 1024
+    // 15.1 (17.9), 8192 x 2048 24.9 (27.0), 4096 x 4096 25.1 = 4.7 TB/s (26.1), 1 x 4096
+    // 3.1 (3.5), 4096 x 8192 45.9 = 5.1 TB/s (47.3), 2048 x 16384 47.9 (52.3), 1024 x
+    // 32768 57.1 (96).  Without a residual a thread of 256 has the loads of two
+    // chunks to keep going: 4096 x 4096 13.0 against 15.0 with 512.
+    const int64_t K = a.K;
+    if (K <= 512)
+        return launch_norm<64, 1>(a, type, s);
+    if (K <= 1024)
+        return launch_norm<64, 2>(a, type, s);
+    if (K <= 2048)
+        return launch_norm<256, 1>(a, type, s);
+    if (K <= 4096)
+        return a.R ? launch_norm<512, 1>(a, type, s) : launch_norm<256, 2>(a, type, s);
+    if (K <= 8192)
+        return launch_norm<512, 2>(a, type, s);
+    if (K <= 16384)
+        return launch_norm<1024, 2>(a, type, s);
+    if (K <= 32768)
+        return launch_norm<1024, 4>(a, type, s);
+    if (K <= 65536)
+        return launch_norm<1024, 8>(a, type, s);
     return launch_norm<1024, 17>(a, type, s);   // 17 * 1024 chunks: every supported K
 }
 

@@ -9,6 +9,7 @@ passes none) and the current stream.  There is no fallback: if the library is
 not built, or a call returns an error status, these functions raise.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -597,7 +598,9 @@ _T16 = (torch.float16, torch.bfloat16)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _SCALES = (torch.uint8, torch.float8_e8m0fnu)
 _U8 = torch.uint8
+_empty_like, _empty_strided = torch.empty_like, torch.empty_strided
 _current_device = torch.cuda.current_device
+_current_stream = torch._C._cuda_getCurrentRawStream   # its handle, by device index
 
 
 def llmint8_b128_pitch(K):
@@ -631,14 +634,18 @@ def _ok(dev, t, name, dtypes, shape):
 def _launch(fn, dev, *args):
     """Calls the library with the stream of device `dev` as the last argument
     (a stream handle belongs to its device, which has to be current)."""
-    f = getattr(_load(), fn)
+    f = getattr(_lib or _load(), fn)
     if _current_device() == dev:
-        rc = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+        rc = f(*args, _current_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = f(*args, _current_stream(dev))
     if rc != LLMINT8_OK:
         raise LLMInt8Error(fn, rc)
+
+
+def _matrix(rows, cols, dtype, device):
+    return _empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
 def llmint8_rmsnorm_b128(X, gamma, eps=1e-6, residual=None, residual_out=None, Y=None, Xq8=None,
@@ -650,7 +657,7 @@ def llmint8_rmsnorm_b128(X, gamma, eps=1e-6, residual=None, residual_out=None, Y
     [T,K] that also receives the normalized rows in X's dtype."""
     shape = _sizes(X, "X", _T16, 2)
     T, K = shape
-    d, dev, dt = X.device, X.get_device(), (X.dtype,)
+    dev, dt = X.get_device(), (X.dtype,)
     ok = _ok(dev, gamma, "gamma", dt, (K,)) & (dev >= 0)
     if residual is not None:
         ok &= _ok(dev, residual, "residual", dt, shape)
@@ -668,11 +675,11 @@ def llmint8_rmsnorm_b128(X, gamma, eps=1e-6, residual=None, residual_out=None, Y
         _on_device(X=X, gamma=gamma, residual=residual, residual_out=residual_out, Y=Y, Xq8=Xq8,
                    SX=SX)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(X)
+        residual_out = _empty_like(X)
     if Xq8 is None:
-        Xq8 = torch.empty(shape, dtype=_U8, device=d)
+        Xq8 = _empty_like(X, dtype=_U8)
     if SX is None:
-        SX = torch.empty((T, _pitch(K)), dtype=_U8, device=d)
+        SX = _matrix(T, _pitch(K), _U8, X.device)
     _launch("llmint8_rmsnorm_b128", dev, X.data_ptr(), _ptr(residual), gamma.data_ptr(),
             _TYPES[X.dtype], T, K, eps, Xq8.data_ptr(), SX.data_ptr(), _ptr(residual_out), _ptr(Y))
     return Xq8, SX, residual_out
@@ -683,7 +690,7 @@ def llmint8_quantize_act_b128(X, Xq8=None, SX=None):
     its 1 x 128 blocks)."""
     shape = _sizes(X, "X", _T16, 2)
     T, K = shape
-    d, dev = X.device, X.get_device()
+    dev = X.get_device()
     ok = dev >= 0
     if Xq8 is not None:
         ok &= _ok(dev, Xq8, "Xq8", _CODES, shape)
@@ -692,9 +699,9 @@ def llmint8_quantize_act_b128(X, Xq8=None, SX=None):
     if not ok:
         _on_device(X=X, Xq8=Xq8, SX=SX)
     if Xq8 is None:
-        Xq8 = torch.empty(shape, dtype=_U8, device=d)
+        Xq8 = _empty_like(X, dtype=_U8)
     if SX is None:
-        SX = torch.empty((T, _pitch(K)), dtype=_U8, device=d)
+        SX = _matrix(T, _pitch(K), _U8, X.device)
     _launch("llmint8_quantize_act_b128", dev, X.data_ptr(), _TYPES[X.dtype], T, K, Xq8.data_ptr(),
             SX.data_ptr())
     return Xq8, SX
@@ -750,8 +757,14 @@ def _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, lead, offsets, row_id
         _on_device(Xq8=Xq8, SX=SX, CB8=CB8, SB=SB, offsets=offsets, row_idx=row_idx, bias=bias,
                    out=out, ws=ws)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=Xq8.device)
+        out = _matrix(M, N, out_dtype, Xq8.device)
     return T, K, N, M, dev, out
+
+
+@functools.lru_cache(maxsize=4096)
+def _b128_need(T, K, N, path, parts):
+    """The workspace query, a pure function of the sizes."""
+    return llmint8_matmul_b128_workspace_bytes(T, K, N, path, parts)
 
 
 def llmint8_matmul_b128_workspace_bytes(T, K, N, path=0, parts=0):
@@ -765,7 +778,7 @@ def llmint8_matmul_b128_path(Xq8, SX, CB8, SB, bias=None, activation=ACT_NONE, o
     T, K, N, _, dev, out = _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, (), None, None,
                                           ws)
     if ws is None:
-        need = _load().llmint8_matmul_b128_workspace_bytes_path(T, K, N, path, parts)
+        need = _b128_need(T, K, N, path, parts)
         if need:
             ws = torch.empty((need,), dtype=_U8, device=Xq8.device)
     _launch("llmint8_matmul_b128_path", dev, Xq8.data_ptr(), SX.data_ptr(), T, K, N,
