@@ -17,7 +17,9 @@ expansion layers.  `quant` selects the 8-bit part's quantizer: "absmax" (the
 method's vector-wise absmax int8), or the library's two variants,
 "zeropoint" (asymmetric int8, llmint8_matmul_zp), "fp8" (E5M2,
 llmint8_matmul_f8) and "fp8_e4m3" (E4M3, llmint8_matmul_e4m3); the variants
-have no fused activation.  This module only holds the tensors, flattens leading
+have no fused activation.  "fp8_block" takes no columns out: weight and input
+are E4M3 with a scale per block of 128 (llmint8_quantize_act_b128 and
+llmint8_matmul_b128, with the fused activation; `threshold` is not used).  This module only holds the tensors, flattens leading
 dimensions into rows, and shares one workspace buffer per (device, stream)
 among all instances, grown as needed, so that steady-state calls allocate
 nothing but their output and a model needs one workspace, not one per layer.
@@ -43,7 +45,7 @@ def _shared_workspace(nbytes, device):
     return ws
 
 _ACTS = {None: L.ACT_NONE, "none": L.ACT_NONE, "relu": L.ACT_RELU}
-_QUANTS = ("absmax", "zeropoint", "fp8", "fp8_e4m3")
+_QUANTS = ("absmax", "zeropoint", "fp8", "fp8_e4m3", "fp8_block")
 # the FP8 quantizers: the binding's function-name suffix of each format
 _FP8 = {"fp8": "f8", "fp8_e4m3": "e4m3"}
 
@@ -61,7 +63,7 @@ class Linear8bitLt(torch.nn.Module):
         super().__init__()
         if quant not in _QUANTS:
             raise ValueError("quant must be one of %s, got %r" % (_QUANTS, quant))
-        if quant != "absmax" and _ACTS.get(activation, None) not in (L.ACT_NONE,):
+        if quant not in ("absmax", "fp8_block") and _ACTS.get(activation, None) not in (L.ACT_NONE,):
             raise ValueError("the %s variant has no fused activation" % quant)
         if quant == "zeropoint" and in_features > 33286:
             raise ValueError("in_features must be at most 33286 for the zero-point variant")
@@ -91,7 +93,8 @@ class Linear8bitLt(torch.nn.Module):
         else:
             self.register_parameter("bias", None)
         self.register_buffer("CB", None)    # int8 codes (fp8 / fp8_e4m3: E5M2 / E4M3 codes, uint8)
-        self.register_buffer("SCB", None)   # absmax: column absmax; zero-point: nd; fp8: 2^-e
+        self.register_buffer("SCB", None)   # absmax: column absmax; zero-point: nd; fp8: 2^-e;
+                                            # fp8_block: E8M0 bytes per block, uint8
         self.register_buffer("ZP", None)    # zero-point variant: zero points and code sums
         self.register_buffer("RS", None)
 
@@ -119,6 +122,13 @@ class Linear8bitLt(torch.nn.Module):
         if self.weight.device.type != "cuda":
             raise RuntimeError("Linear8bitLt: move the module to a HIP device before quantizing")
         w = self.weight.detach().contiguous()
+        if self.quant == "fp8_block":
+            same = self.CB is not None and self.CB.device == w.device
+            self.CB, self.SCB = L.llmint8_quantize_weight_b128(
+                w, CB8=self.CB if same else None, SB=self.SCB if same else None)
+            if not self.has_fp16_weights:
+                self.weight = None
+            return self
         if self.CB is None or self.CB.device != w.device:
             dt = torch.uint8 if self.quant in _FP8 else torch.int8
             self.CB = torch.empty((self.out_features, self.in_features), dtype=dt, device=w.device)
@@ -140,6 +150,20 @@ class Linear8bitLt(torch.nn.Module):
         return _shared_workspace(L.llmint8_workspace_bytes(T, self.in_features, self.out_features),
                                  device)
 
+    def _forward_block(self, x2):
+        """The block-scaled product of x2 [T,K]: its codes, their scales and the
+        product's workspace are parts of the shared workspace."""
+        T, K = x2.shape
+        codes, scales = T * K, T * L.llmint8_b128_pitch(K)
+        first = codes + (scales + 255) // 256 * 256
+        need = L.llmint8_matmul_b128_workspace_bytes(T, K, self.out_features)
+        ws = _shared_workspace(first + need, x2.device)
+        Xq8, SX = L.llmint8_quantize_act_b128(x2, Xq8=ws[:codes].view(T, K),
+                                              SX=ws[codes:codes + scales].view(T, -1))
+        return L.llmint8_matmul_b128(Xq8, SX, self.CB, self.SCB, bias=self.bias,
+                                     activation=_ACTS[self.activation],
+                                     ws=ws[first:first + need] if need else None)
+
     def forward(self, x):
         if x.dtype != torch.float16:
             raise TypeError("Linear8bitLt expects fp16 input, got %s" % x.dtype)
@@ -153,6 +177,8 @@ class Linear8bitLt(torch.nn.Module):
         T = x2.shape[0]
         if T == 0:
             return x.new_empty(lead + (self.out_features,))
+        if self.quant == "fp8_block":
+            return self._forward_block(x2).reshape(lead + (self.out_features,))
         ws = self._workspace(T, x2.device)
         if self.quant == "zeropoint":
             out = L.llmint8_matmul_zp(x2, self.CB, self.SCB, self.ZP, self.RS, self.threshold,
