@@ -39,6 +39,19 @@ __device__ __forceinline__ uint16_t f2t(float f)
         return f2h(f);
 }
 
+// Two values side by side (one conversion instruction where there is one).
+template <int kT>
+__device__ __forceinline__ unsigned pack2(float a, float b)
+{
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    if constexpr (kT == kTypeBf16)
+        return __builtin_bit_cast(unsigned, __builtin_convertvector((f2{a, b}), b2));
+    else
+        return __builtin_bit_cast(unsigned, __builtin_convertvector((f2{a, b}), h2));
+}
+
 // The scale of a block whose largest magnitude has the fp32 bits `a` (sign
 // clear): e is the largest integer with a * 2^e <= 448 = 1.75 * 2^8, at most
 // 126 so that the stored 2^-e stays a normal fp32; 0 for a = 0.  With

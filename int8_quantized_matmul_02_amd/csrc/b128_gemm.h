@@ -187,8 +187,7 @@ __device__ __forceinline__ uint2 finish4(v4f v, float lowest)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
         v[q] = __builtin_elementwise_maximum(v[q], lowest);
-    return make_uint2(f2t<kT>(v[0]) | (unsigned)f2t<kT>(v[1]) << 16,
-                      f2t<kT>(v[2]) | (unsigned)f2t<kT>(v[3]) << 16);
+    return make_uint2(pack2<kT>(v[0], v[1]), pack2<kT>(v[2], v[3]));
 }
 // Four bias values (zeros without a bias).
 template <int kT>
@@ -466,8 +465,8 @@ struct BigCfg {
     static constexpr int kChunk = 16;                          // stages per chunk of scales
     static constexpr int kScaleRows = BM * kChunk;             // then 256 bytes per wavefront: its columns'
     static constexpr int kScaleBytes = kScaleRows + kWaves * 256;
-    static constexpr int kOut = kRing + 2 * kScaleBytes;
-    static constexpr int kLdsBytes = kOut + kWaves * kOutBytes;
+    static constexpr int kStaging = kRing + 2 * kScaleBytes;
+    static constexpr int kLdsBytes = kStaging + kWaves * kOutBytes;
     static constexpr int kPerCu = 160 * 1024 / kLdsBytes;      // resident blocks per CU
     // the stage's schedule, in MFMAs
     static constexpr int kMfmas = FM * FN, kPair = 2 * FN, kPairs = FM / 2;
@@ -602,27 +601,42 @@ __device__ __forceinline__ void store_tile(const B128Args &a, const Tile &t,
     for (int q = 0; q < 16 / C::kRowsPerStore; ++q)
         off[q] = nw + 8 * pc < a.N ? (uint32_t)((q * C::kRowsPerStore + pr) * a.N * 2 + 16 * pc)
                                    : kNowhere;
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
+    const int64_t inside = nw < a.N;
+    // While row tile i's pieces come back from LDS, tile i + 1 is converted.
+    uint2 o[C::FN];
+    auto convert = [&](int i) {
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
             pin(acc[i][j]);   // stays an accumulator register until its turn
-            *reinterpret_cast<uint2 *>(put[j]) = finish4<kT>(acc[i][j], lowest);
+            o[j] = finish4<kT>(acc[i][j], lowest);
         }
+    };
+    convert(0);
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+            *reinterpret_cast<uint2 *>(put[j]) = o[j];
         __builtin_amdgcn_wave_barrier();
-        const int64_t row = t.m0 + wm * C::kTM + i * 16, left = t.mend - row;
-        const __amdgpu_buffer_rsrc_t out = resource(
-            reinterpret_cast<const uint8_t *>(a.out + row * a.N + nw),
-            left > 0 && nw < a.N ? (left * a.N - nw) * 2 : 0);
+        uint4 w[16 / C::kRowsPerStore];
 #pragma unroll
         for (int q = 0; q < 16 / C::kRowsPerStore; ++q) {
             const int x = q * C::kRowsPerStore + pr;
-            buf_store16(*reinterpret_cast<const uint4 *>(st + x * (C::kTN * 2) +
-                                                         16 * (pc ^ (x & (kMask >> 1)))),
-                        out, off[q]);
+            w[q] = *reinterpret_cast<const uint4 *>(st + x * (C::kTN * 2) +
+                                                    16 * (pc ^ (x & (kMask >> 1))));
         }
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_sched_barrier(0);
+        if (i + 1 < C::FM)
+            convert(i + 1);
+        const int64_t row = t.m0 + wm * C::kTM + i * 16, left = t.mend - row;
+        const __amdgpu_buffer_rsrc_t out = resource(
+            reinterpret_cast<const uint8_t *>(a.out + row * a.N + nw),
+            max(left * a.N - nw, (int64_t)0) * (2 * inside));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < 16 / C::kRowsPerStore; ++q)
+            buf_store16(w[q], out, off[q]);
     }
 }
 
@@ -646,7 +660,11 @@ __device__ __forceinline__ void store_parts(const B128Args &a, const Tile &t,
     }
 }
 
-template <class C, bool kGather>
+// kOut: the output's element type, or kOutParts for the fp32 sums of a part of
+// K.  (A branch on it in one kernel costs copies of the accumulators.)
+constexpr int kOutParts = 2;
+
+template <class C, bool kGather, int kOut>
 __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
 {
     __shared__ __attribute__((aligned(1024))) char smem[C::kLdsBytes];
@@ -708,7 +726,7 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
             bias[j] = make_uint2(0, 0);
-            if (a.bias && !a.parts)
+            if (kOut != kOutParts && a.bias)
                 bias[j] = *reinterpret_cast<const uint2 *>(
                     a.bias + (int64_t)t.e * a.N +
                     min(t.n0 + wn * C::kTN + j * 16 + 4 * g, a.N - 4));
@@ -736,14 +754,18 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
     for (bool first = true;; first = false) {
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
-            const v4f b = a.type == kTypeBf16 ? bias4<kTypeBf16>(bias[j]) : bias4<kTypeF16>(bias[j]);
+            v4f b = {0, 0, 0, 0};
+            if constexpr (kOut != kOutParts)
+                b = bias4<kOut>(bias[j]);
 #pragma unroll
-            for (int i = 0; i < C::FM; ++i)
+            for (int i = 0; i < C::FM; ++i) {
                 acc[i][j] = b;
+                pin(acc[i][j]);
+            }
         }
         // The first stage and scales have landed; its fragments, but for A's
         // last pair.  The stores of the tile before are younger and may go on.
-        if (first || a.parts)
+        if (first || kOut == kOutParts)
             wait_vm<(C::STAGES - 1) * C::kLoads>();
         else
             wait_vm<(C::STAGES - 1) * C::kLoads + C::kStores>();
@@ -805,14 +827,10 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
             t = tiles.find(a, v, lane);
             start();
         }
-        if (a.parts)
+        if constexpr (kOut == kOutParts)
             store_parts<C>(a, done, acc, wm, wn, lane);
-        else if (a.type == kTypeBf16)
-            store_tile<C, kTypeBf16>(a, done, acc, smem + C::kOut + wave * C::kOutBytes, wm, wn,
-                                     lane);
         else
-            store_tile<C, kTypeF16>(a, done, acc, smem + C::kOut + wave * C::kOutBytes, wm, wn,
-                                    lane);
+            store_tile<C, kOut>(a, done, acc, smem + C::kStaging + wave * C::kOutBytes, wm, wn, lane);
         if (v >= count)
             break;
     }
@@ -872,10 +890,16 @@ hipError_t launch_big(const B128Args &a, hipStream_t s)
     if (n > 0x7fffffff)
         return hipErrorInvalidValue;
     const dim3 grid((unsigned)(n < kResident ? n : kResident));
-    if (a.row_idx)
-        hipLaunchKernelGGL((k_b128_big<C, true>), grid, dim3(C::kThreads), 0, s, a);
+    if (a.parts)
+        hipLaunchKernelGGL((k_b128_big<C, false, kOutParts>), grid, dim3(C::kThreads), 0, s, a);
+    else if (a.row_idx && a.type == kTypeBf16)
+        hipLaunchKernelGGL((k_b128_big<C, true, kTypeBf16>), grid, dim3(C::kThreads), 0, s, a);
+    else if (a.row_idx)
+        hipLaunchKernelGGL((k_b128_big<C, true, kTypeF16>), grid, dim3(C::kThreads), 0, s, a);
+    else if (a.type == kTypeBf16)
+        hipLaunchKernelGGL((k_b128_big<C, false, kTypeBf16>), grid, dim3(C::kThreads), 0, s, a);
     else
-        hipLaunchKernelGGL((k_b128_big<C, false>), grid, dim3(C::kThreads), 0, s, a);
+        hipLaunchKernelGGL((k_b128_big<C, false, kTypeF16>), grid, dim3(C::kThreads), 0, s, a);
     return hipGetLastError();
 }
 

@@ -44,7 +44,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
     unsigned w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = (unsigned)f2t<kT>(f[2 * i]) | ((unsigned)f2t<kT>(f[2 * i + 1]) << 16);
+        w[i] = pack2<kT>(f[2 * i], f[2 * i + 1]);
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
