@@ -465,7 +465,7 @@ LLMINT8_API llmint8_status_t llmint8_matmul_b128(const uint8_t *Xq8, const uint8
  * The group sizes stay on the device: nothing is copied to the host.  Offsets
  * outside [0, M] and indices outside [0, T) are taken as the nearest bound
  * (no access leaves the arrays); decreasing offsets give unspecified rows.
- * With row_idx, T * K < 2^32 (else LLMINT8_ERR_UNSUPPORTED_SHAPE).
+ * With row_idx, T * K <= 2^32 - 2^21 (else LLMINT8_ERR_UNSUPPORTED_SHAPE).
  */
 LLMINT8_API llmint8_status_t llmint8_matmul_grouped_b128(
     const uint8_t *Xq8, const uint8_t *SX, int64_t T, int64_t K, int64_t N, const uint8_t *CB8,

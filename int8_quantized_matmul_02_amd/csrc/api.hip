@@ -179,7 +179,7 @@ const char *llmint8_status_string(int status)
     switch (status) {
     case LLMINT8_OK: return "LLMINT8_OK";
     case LLMINT8_ERR_INVALID_ARG: return "LLMINT8_ERR_INVALID_ARG: null/misaligned pointer, non-positive size or NaN/negative threshold";
-    case LLMINT8_ERR_UNSUPPORTED_SHAPE: return "LLMINT8_ERR_UNSUPPORTED_SHAPE: K and N must be multiples of 64, K <= 133144 (K <= 33286 for the zero-point variant; T <= 16 for the weight-streaming path)";
+    case LLMINT8_ERR_UNSUPPORTED_SHAPE: return "LLMINT8_ERR_UNSUPPORTED_SHAPE: K and N must be multiples of 64, K <= 133144 (K <= 33286 for the zero-point variant; T <= 16 for the weight-streaming path; further limits of the block-scaled operators: see llmint8.h)";
     case LLMINT8_ERR_WORKSPACE: return "LLMINT8_ERR_WORKSPACE: workspace smaller than the size query";
     case LLMINT8_ERR_HIP: return "LLMINT8_ERR_HIP: a kernel launch failed";
     case LLMINT8_ERR_SCRATCH: return "LLMINT8_ERR_SCRATCH: the call needs more workspace than the static scratch of llmint8_matmul_noalloc (LLMINT8_NOALLOC_SCRATCH_BYTES = 64 MiB)";

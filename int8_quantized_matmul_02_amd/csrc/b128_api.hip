@@ -26,6 +26,7 @@ constexpr int64_t kMaxRows = 0x7fff0000;
 constexpr int64_t kMaxB128K = 133144;
 constexpr int64_t kMaxB128N = (int64_t)1 << 24;
 constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxIndexedBytes = 0xffe00000;   // what a buffer resource covers
 constexpr int64_t kMaxOutputs = (int64_t)1 << 38;   // of one product: 512 GB, past the card's memory
 
 llmint8_status_t check_b128(int64_t T, int64_t K, int64_t N, int64_t E)
@@ -164,7 +165,7 @@ llmint8_status_t llmint8_matmul_grouped_b128_path(const uint8_t *Xq8, const uint
     if (st != LLMINT8_OK)
         return st;
     // rows read by index are addressed with 32-bit offsets
-    if (M > kMaxRows || M * N > kMaxOutputs || (row_idx && T * K > 0xffffffffll))
+    if (M > kMaxRows || M * N > kMaxOutputs || (row_idx && T * K > kMaxIndexedBytes))
         return LLMINT8_ERR_UNSUPPORTED_SHAPE;
     return status(launch_matmul_b128(B128Args{Xq8, SX, CB8, SB, bias, out, T, M, K, N, activation,
                                               type, (int)E, offsets, row_idx},

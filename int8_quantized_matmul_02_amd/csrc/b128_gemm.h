@@ -127,6 +127,10 @@ struct Tiles {
             }
             before += __builtin_amdgcn_readlane(s0, kWave - 1);
             base += kWave;
+            if (base >= a.E) {   // only if the offsets changed meanwhile: a tile without rows
+                t.m0 = t.mend = 0;
+                return t;
+            }
             o0 = group_tiles(a, base, lane, BM, l0, h0);
             s0 = wave_prefix_sum(o0);
         }
@@ -136,7 +140,7 @@ struct Tiles {
 // The activation row of output row i (rows past the group's end: its last).
 __device__ __forceinline__ int64_t source_row(const B128Args &a, const Tile &t, int64_t i)
 {
-    i = i < t.mend ? i : t.mend - 1;
+    i = i < t.mend ? i : t.mend > 0 ? t.mend - 1 : 0;
     if (a.row_idx) {
         const int64_t r = a.row_idx[i];
         return r < 0 ? 0 : r < a.rows ? r : a.rows - 1;

@@ -39,20 +39,21 @@ struct Shape {
     int resident;         // blocks per compute unit
     double in_flight;     // bytes a block keeps on their way
     double fixed, pace;   // pace: us per block of K at the least
+    bool persistent;      // blocks take several tiles
     hipError_t (*launch)(const B128Args &, hipStream_t);
 };
 template <class C>
 constexpr Shape small_shape()
 {
     return {C::BM, C::BN, 160 * 1024 / C::kLdsBytes, (C::STAGES - 1.0) * (C::BM + C::BN) * C::kRowB,
-            1.0, 0.0, b128::launch_small<C>};
+            1.0, 0.0, false, b128::launch_small<C>};
 }
 template <class C>
 constexpr Shape big_shape(double fixed, double pace)
 {
     // the buffer of the stage being multiplied is refilled early on
     return {C::BM, C::BN, C::kPerCu, (C::STAGES - 0.3) * C::kStageBytes, fixed, pace,
-            b128::launch_big<C>};
+            true, b128::launch_big<C>};
 }
 const Shape kShapes[kB128Paths] = {
     small_shape<Small16x16>(),   small_shape<Small16x32>(), small_shape<Small16x32s2>(),
@@ -97,6 +98,8 @@ Plan choose(int64_t M, int64_t K, int64_t N, int64_t E, bool grouped, int path, 
                 break;
             const int per = (int)((nblk + parts - 1) / parts + 3) / 4 * 4;   // whole dwords of scales
             const int n = (int)((nblk + per - 1) / per);
+            if (!path && !s.persistent && tiles * n * 512 >= 0x1p32)
+                break;   // a launch has fewer than 2^32 threads
             const double per_cu = __builtin_ceil(tiles * n / kCUs);
             const double here = per_cu < s.resident ? per_cu : s.resident;
             double rate = here * s.in_flight / kLatency;

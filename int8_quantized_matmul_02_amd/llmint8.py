@@ -680,8 +680,10 @@ def llmint8_rmsnorm_b128(X, gamma, eps=1e-6, residual=None, residual_out=None, Y
         Xq8 = _empty_like(X, dtype=_U8)
     if SX is None:
         SX = _matrix(T, _pitch(K), _U8, X.device)
-    _launch("llmint8_rmsnorm_b128", dev, X.data_ptr(), _ptr(residual), gamma.data_ptr(),
-            _TYPES[X.dtype], T, K, eps, Xq8.data_ptr(), SX.data_ptr(), _ptr(residual_out), _ptr(Y))
+    if T:
+        _launch("llmint8_rmsnorm_b128", dev, X.data_ptr(), _ptr(residual), gamma.data_ptr(),
+                _TYPES[X.dtype], T, K, eps, Xq8.data_ptr(), SX.data_ptr(), _ptr(residual_out),
+                _ptr(Y))
     return Xq8, SX, residual_out
 
 
@@ -702,8 +704,9 @@ def llmint8_quantize_act_b128(X, Xq8=None, SX=None):
         Xq8 = _empty_like(X, dtype=_U8)
     if SX is None:
         SX = _matrix(T, _pitch(K), _U8, X.device)
-    _launch("llmint8_quantize_act_b128", dev, X.data_ptr(), _TYPES[X.dtype], T, K, Xq8.data_ptr(),
-            SX.data_ptr())
+    if T:
+        _launch("llmint8_quantize_act_b128", dev, X.data_ptr(), _TYPES[X.dtype], T, K,
+                Xq8.data_ptr(), SX.data_ptr())
     return Xq8, SX
 
 
@@ -777,6 +780,8 @@ def llmint8_matmul_b128_path(Xq8, SX, CB8, SB, bias=None, activation=ACT_NONE, o
     chosen; 0 leaves the choice to the library."""
     T, K, N, _, dev, out = _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, (), None, None,
                                           ws)
+    if T == 0:
+        return out
     if ws is None:
         need = _b128_need(T, K, N, path, parts)
         if need:

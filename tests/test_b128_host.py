@@ -89,7 +89,8 @@ def test_grouped_refusals(lib):
                dict(T=0, M=0)):
         assert f(**kw) == 1, kw
     for kw in (dict(E=1025), dict(K=96), dict(N=32), dict(idx=P, M=1 << 31),
-               dict(idx=P, T=1 << 25, K=128), dict(idx=P, M=1 << 30, N=1 << 10)):
+               dict(idx=P, T=1 << 25, K=128),
+               dict(idx=P, T=(1 << 25) - (1 << 13), K=128), dict(idx=P, M=1 << 30, N=1 << 10)):
         assert f(**kw) == 2, kw
 
 

@@ -422,6 +422,34 @@ def test_grouped_without_rows():
     assert r.shape == (0, 64)
 
 
+def test_no_rows():
+    d = dev()
+    X, g = torch.empty((0, 192), dtype=torch.float16, device=d), torch.ones(192, dtype=torch.float16, device=d)
+    q, s, h = L.llmint8_rmsnorm_b128(X, g, residual=X)
+    assert q.shape == h.shape == (0, 192) and s.shape == (0, 4)
+    q, s = L.llmint8_quantize_act_b128(X)
+    _, _, wq, sw = up(*operands(1, 192, 64, 1))
+    assert L.llmint8_matmul_b128(q, s, wq, sw).shape == (0, 64)
+
+
+@pytest.mark.parametrize("path", [0, 1, 5, 8, 9])
+@pytest.mark.parametrize("E", [3, 70])
+def test_grouped_bounds(E, path):
+    """Offsets outside [0, M] and indices outside [0, T) count as the nearest bound."""
+    d, T, K, N, M = dev(), 9, 192, 128, 40
+    xq, sx, wq, sw = operands(T, K, N, 5, E=E, exact=True)
+    off = np.concatenate([[-7, 11, 11], np.full(E - 3, 11), [4000]]).astype(np.int32)
+    off[E - 1] = 25
+    idx = np.random.default_rng(3).integers(-20, 30, M).astype(np.int32)
+    out = torch.full((M, N), 9.0, dtype=torch.float16, device=d)
+    L.llmint8.llmint8_matmul_grouped_b128_path(*up(xq, sx, wq, sw, off), row_idx=up(idx)[0], out=out,
+                                               path=path)
+    x, b = ref.values(xq, sx, 1)[idx.clip(0, T - 1)], off.clip(0, M)
+    for e in range(E):
+        v, S = expect(x[b[e]:b[e + 1]], ref.values(wq[e], sw[e], 128), None, False)
+        check_product(out[b[e]:b[e + 1]], v, S, K, torch.float16, True, "expert %d" % e)
+
+
 def test_grouped_equals_single_products():
     """One expert's rows give the bits of the plain product's, and a row does
     not depend on the others of its group."""
