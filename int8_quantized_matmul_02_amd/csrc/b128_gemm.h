@@ -97,9 +97,9 @@ struct Tiles {
     }
     __device__ __forceinline__ int count(const B128Args &a) const { return ntm * ntn * a.nparts; }
 
-    // Tile v < count(), the parts of K one after another: workgroup ids are dealt round-robin over the XCDs, so
-    // each XCD takes a contiguous run of tiles, which walk GROUP tile rows at
-    // a time.
+    // Tile v < count(), the parts of K one after another: workgroup ids are
+    // dealt round-robin over the XCDs, so each XCD takes a contiguous run of
+    // tiles, which walk GROUP tile rows at a time.
     __device__ __forceinline__ Tile find(const B128Args &a, int v, int lane) const
     {
         Tile t;
@@ -127,8 +127,8 @@ struct Tiles {
             }
             before += __builtin_amdgcn_readlane(s0, kWave - 1);
             base += kWave;
-            if (base >= a.E) {   // only if the offsets changed meanwhile: a tile without rows
-                t.m0 = t.mend = 0;
+            if (base >= a.E) {   // only if the offsets changed meanwhile: a tile without work
+                t.m0 = t.mend = t.nk = 0;
                 return t;
             }
             o0 = group_tiles(a, base, lane, BM, l0, h0);
@@ -254,6 +254,8 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
     if ((int)blockIdx.x >= tiles.count(a))
         return;
     const Tile t = tiles.find(a, blockIdx.x, lane);
+    if (t.nk == 0)
+        return;
     const int wn = wave % C::WN, wm = wave / C::WN % C::WM, wk = wave / (C::WN * C::WM);
     const int64_t pitch = b128_pitch(a.K);
     const int nst = (t.nk + 3) / 4;   // stages of four blocks

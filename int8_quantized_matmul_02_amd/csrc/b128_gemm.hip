@@ -19,21 +19,22 @@ using Big256 = b128::BigCfg<256, 256, 2, 2, 2, 4>;
 namespace {
 
 // The tile and the parts of K are those with the least estimated time.  In
-// microseconds, with what sweeps over 139 sizes on MI355X showed:
+// microseconds, with constants fitted to sweeps over 630 plain and grouped
+// sizes on MI355X, each with all shapes that could matter and 1, 2, 4 or 8 parts:
 //   * a block reads (BM + BN) * K bytes at what its compute unit draws: the
-//     bytes its resident blocks keep in flight over 0.9 us of latency, at most
-//     57 KB/us (all units together 14.6 TB/s, from L2);
-//   * 256 x 256 is bound by the matrix cores instead, 1.5 us per block of K;
+//     bytes its resident blocks keep in flight over 0.5 us of latency, at most
+//     68 KB/us;
+//   * 256 x 256 is bound by the matrix cores instead, 1.15 us per block of K;
 //   * a block costs `fixed` besides, shared by those resident together;
-//   * the weight comes from HBM at 5 TB/s; the longer of reading it and of the
-//     blocks counts whole, the shorter for three quarters (they overlap in part);
-//   * a split of K adds a launch and its partial sums, written and read.
-// Over the sweep the choice took 2.7 % longer than the best of 16 shapes with
-// 1, 2, 4 or 8 parts (geometric mean; these nine shapes at best 0.5 %).  Some
-// of it, in us: 1 x 4096 x 16384 16 x 64 16.2, 16 x 16 17.6; 1 x 16384 x 4096 16 x 16 15.0,
-// 16 x 64 23.7; 64 experts with a row or two, K = 2048, N = 1024: 16 x 32 20.4, 16 x 16
-// 31.3; 300 x 2048 x 8192: 128 x 128 12.8, 64 x 128 15.4; 256 x 16384 x 4096: 128 x 128 in
-// 4 parts 36, whole 90; 4096 x 4096 x 16384: 256 x 256 208, 128 x 128 349.
+//   * the weight, read from HBM rather than L2, adds its bytes at 12 TB/s;
+//   * a split of K adds a launch and its partial sums, written and read;
+//   * an expert's last tile, on average, wastes 0.6 of its rows.
+// The choice takes 1.3 % longer than the best of them (geometric mean; grouped
+// 1.6 %, whose row counts the host does not know).  Some of the sweep, in us:
+// 1 x 4096 x 16384: 16 x 32 13.9, 16 x 16 15.6; 1 x 16384 x 4096: 16 x 16 14.2, 16 x 32
+// 16.1; 300 x 2048 x 8192: 128 x 128 12.8, 64 x 128 15.2; 256 x 16384 x 4096: 128 x 128
+// in 4 parts 36.5, 64 x 64 whole 42.8; 4096 x 4096 x 16384: 256 x 256 209, 128 x 128 277;
+// 2222 rows of 8 experts, K = N = 4096: 256 x 256 58, 128 x 128 71.
 struct Shape {
     int bm, bn;
     int resident;         // blocks per compute unit
@@ -46,7 +47,7 @@ template <class C>
 constexpr Shape small_shape()
 {
     return {C::BM, C::BN, 160 * 1024 / C::kLdsBytes, (C::STAGES - 1.0) * (C::BM + C::BN) * C::kRowB,
-            1.0, 0.0, false, b128::launch_small<C>};
+            3.6, 0.0, false, b128::launch_small<C>};
 }
 template <class C>
 constexpr Shape big_shape(double fixed, double pace)
@@ -58,9 +59,9 @@ constexpr Shape big_shape(double fixed, double pace)
 const Shape kShapes[kB128Paths] = {
     small_shape<Small16x16>(),   small_shape<Small16x32>(), small_shape<Small16x32s2>(),
     small_shape<Small16x64>(),   small_shape<Small32x64>(), small_shape<Small64x64>(),
-    big_shape<Big64x128>(1.0, 0.0), big_shape<Big128>(1.0, 0.0), big_shape<Big256>(5.0, 1.5),
+    big_shape<Big64x128>(5.2, 0.0), big_shape<Big128>(5.2, 0.0), big_shape<Big256>(11.4, 1.15),
 };
-constexpr double kLatency = 0.9, kCuRate = 57e3, kHbmRate = 5e6, kSumRate = 8e6;   // us, bytes per us
+constexpr double kLatency = 0.5, kCuRate = 68e3, kWeightRate = 12e6, kSumRate = 5.3e6;   // us, bytes per us
 constexpr int kCUs = 256;
 constexpr int64_t kMostParts = (int64_t)128 << 20;   // bytes of partial sums
 
@@ -74,17 +75,17 @@ struct Plan {
 Plan choose(int64_t M, int64_t K, int64_t N, int64_t E, bool grouped, int path, int only)
 {
     const int64_t nblk = (K + kB128 - 1) / kB128, used = E < M ? E : M;
-    const double hbm = (double)(grouped ? used : 1) * N * K / kHbmRate;
+    const double weight = (double)(grouped ? used : 1) * N * K / kWeightRate;
     Plan best{&kShapes[0], 1, (int)nblk};
     double least = 1e300;
     for (int i = 0; i < kB128Paths; ++i) {
         const Shape &s = kShapes[i];
         if (path && path != i + 1)
             continue;
-        // rows of tiles: of a grouped product, each expert's last one is half full on average
+        // rows of tiles: of a grouped product, each expert's last one is partly full
         double ntm = (double)((M + s.bm - 1) / s.bm);
         if (grouped) {
-            ntm = (double)M / s.bm + 0.5 * used;
+            ntm = (double)M / s.bm + 0.6 * used;
             ntm = ntm < used ? used : ntm;
         }
         const double tiles = ntm * ((N + s.bn - 1) / s.bn);
@@ -98,7 +99,8 @@ Plan choose(int64_t M, int64_t K, int64_t N, int64_t E, bool grouped, int path, 
                 break;
             const int per = (int)((nblk + parts - 1) / parts + 3) / 4 * 4;   // whole dwords of scales
             const int n = (int)((nblk + per - 1) / per);
-            if (!path && !s.persistent && tiles * n * 512 >= 0x1p32)
+            if (!path && !s.persistent &&
+                ((double)M / s.bm + (grouped ? used : 1)) * ((N + s.bn - 1) / s.bn) * n * 512 >= 0x1p32)
                 break;   // a launch has fewer than 2^32 threads
             const double per_cu = __builtin_ceil(tiles * n / kCUs);
             const double here = per_cu < s.resident ? per_cu : s.resident;
@@ -106,10 +108,9 @@ Plan choose(int64_t M, int64_t K, int64_t N, int64_t E, bool grouped, int path, 
             rate = rate < kCuRate ? rate : kCuRate;
             double one = (rows + s.bn) * per * kB128 / rate;
             one = (one < per * s.pace ? per * s.pace : one) + s.fixed / here;
-            const double blocks = per_cu * one;
-            double t = blocks < hbm ? hbm + 0.75 * blocks : blocks + 0.75 * hbm;
+            double t = per_cu * one + weight;
             if (n > 1)
-                t += 3.0 + 2.0 * n * M * N * 4 / kSumRate;
+                t += 2.8 + 2.0 * n * M * N * 4 / kSumRate;
             if (t < least) {
                 least = t;
                 best = Plan{&s, n, per};
