@@ -218,6 +218,10 @@ __device__ __forceinline__ float lowest_output(const B128Args &a)
 // A lane's 32 bytes of a block are its chunks g and g + 4 (g = lane / 16), the
 // same for both operands; in a last block of 64 columns chunks 4 .. 7 are
 // replaced by zeros.
+//
+// Bound by HBM: one token, K = 4096, N = 16384 takes 14 us = 4.8 TB/s of weight
+// from HBM, 12 with part of it in the last-level cache; 64 experts of 2048 x 1024
+// with one row each 28 us = 4.8 TB/s.
 // ---------------------------------------------------------------------------
 template <int BM_, int BN_, int WM_, int WN_, int WK_, int STAGES_>
 struct SmallCfg {
@@ -436,9 +440,19 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
 // stage s + STAGES goes into its buffer, spread over the rest (issued
 // faster, the loads stall in the address unit and the MFMAs behind them);
 // after kLand MFMAs stage s + 1 has landed.  Measured at 4096 x 4096 x 16384,
-// 4096 x 16384 x 4096 and 8192^3: one barrier after the first pair and a load
-// per MFMA 220, 218, 405 us; a load every 2nd 215, 207, 394; two barriers and
-// every 2nd 210, 204, 386; every 3rd 208, 195, 377.
+// 4096 x 16384 x 4096 and 8192^3: a load per MFMA 227, 231, 428 us; before every
+// 2nd 216, 209, 405; every 3rd 214, 197, 400.
+//
+// What bounds it: a stage of 256 x 256 takes 2850 cycles on a compute unit, 2048
+// of them MFMAs (64 of 32 cycles per SIMD), 600 waiting at the two barriers.  With
+// all compute units busy the power limit then holds the clock at 1.8 - 2.0 GHz
+// (alone, a tile runs at 2.37): 4096 x 4096 x 16384 in 214 us = 2570 TFLOP/s,
+// where the library's product of per-tensor scales takes 219; 8192^3 400 us (395).
+// A stage of 128 x 128 takes 1110 cycles against 512 of MFMAs, the transfers into
+// and out of LDS 768; two resident blocks share them.  Deeper rings (128 x 128
+// with 4 stages, 64 x 128 with 6) change nothing there.  Experts' weights come
+// cold, in pieces of 128 bytes a row apart, at up to 4.4 TB/s (pieces of 512: 5.1):
+// 8 x 4096 x 4096 with 64 rows each 38 us = 3.5 TB/s.
 //
 // Blocks are persistent: a block takes tiles v, v + grid, ..., and loads the
 // next tile's first stages before it writes a finished tile out.  Past a
@@ -503,8 +517,8 @@ struct BigCfg {
 
 // Keeps the MFMAs on `v` between the side-effecting operations around this
 // point: an MFMA is a pure value to the compiler, which otherwise gathers a
-// stage's MFMAs in one run and leaves the loads and reads behind it (273 us
-// against 240 at 4096 x 4096 x 16384, in an earlier form of this kernel).
+// stage's MFMAs in one run and leaves the loads and reads behind it (235 us
+// against 214 at 4096 x 4096 x 16384).
 __device__ __forceinline__ void pin(v4f &v) { asm volatile("" : "+a"(v)); }
 
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
@@ -842,7 +856,9 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
     }
 }
 
-// out = act(sum of the parts + bias): 4 outputs per thread.
+// out = act(sum of the parts + bias): 4 outputs per thread.  256 x 4096 outputs of
+// 4 parts take 4.7 us = 4.0 TB/s, the launch included.  (All parts requested at
+// once, before the first addition: 6.9 us.)
 template <int kT>
 __global__ __launch_bounds__(256) void k_b128_sum(B128Args a)
 {
