@@ -19,12 +19,14 @@ method's vector-wise absmax int8), or the library's two variants,
 llmint8_matmul_f8) and "fp8_e4m3" (E4M3, llmint8_matmul_e4m3); the variants
 have no fused activation.  "fp8_block" takes no columns out: weight and input
 are E4M3 with a scale per block of 128 (llmint8_quantize_act_b128 and
-llmint8_matmul_b128, with the fused activation; `threshold` is not used).  This module only holds the tensors, flattens leading
-dimensions into rows, and shares one workspace buffer per (device, stream)
-among all instances, grown as needed, so that steady-state calls allocate
-nothing but their output and a model needs one workspace, not one per layer.
-Calls on one stream run in order, so they may share it; calls on different
-streams get different buffers.
+llmint8_matmul_b128, with the fused activation; `threshold` is not used).
+
+This module only holds the tensors, flattens leading dimensions into rows,
+and shares one workspace buffer per (device, stream) among all instances,
+grown as needed, so that steady-state calls allocate nothing but their output
+and a model needs one workspace, not one per layer.  Calls on one stream run
+in order, so they may share it; calls on different streams get different
+buffers, and calls captured into a graph get theirs from the graph's memory.
 """
 import torch
 
@@ -35,6 +37,10 @@ _WORKSPACES = {}
 
 
 def _shared_workspace(nbytes, device):
+    if torch.cuda.is_current_stream_capturing():
+        # a graph is replayed on any stream, beside other graphs, and outlives
+        # the buffer of its day: its workspace is its own
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
     key = (device, torch.cuda.current_stream(device).cuda_stream)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:

@@ -84,3 +84,41 @@ def test_layers_share_the_workspace_and_streams_do_not():
     torch.cuda.synchronize()
     for i in (0, 1):
         assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+@gpu
+def test_graphs_have_their_own_workspace():
+    """Graphs of layers replay beside each other and beside larger eager calls
+    on the stream that captured them."""
+    d = torch.device("cuda:0")
+    torch.manual_seed(3)
+    m = Linear8bitLt(1088, 320, quant="fp8_block").to(d)
+    xs = [torch.randn(t, 1088).half().to(d) for t in (5, 200, 700)]
+    want = [m(x) for x in xs]
+    s, others = torch.cuda.Stream(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in xs[:2]:
+        with torch.cuda.stream(s):
+            m(x)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            outs.append(m(x))
+    with torch.cuda.stream(s):
+        m(xs[2])       # a larger workspace replaces the stream's
+    torch.cuda.synchronize()
+    kept = [torch.full((1 << n,), 77, dtype=torch.uint8, device=d) for n in range(10, 22)]
+    for _ in range(5):
+        for o in outs:
+            o.fill_(3.0)
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, others):
+            with torch.cuda.stream(st):
+                g.replay()
+        with torch.cuda.stream(s):
+            big = m(xs[2])
+        torch.cuda.synchronize()
+        assert torch.equal(big, want[2])
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+        assert all(bool((k == 77).all()) for k in kept)
