@@ -26,6 +26,7 @@ constexpr int64_t kMaxRows = 0x7fff0000;
 constexpr int64_t kMaxB128K = 133144;
 constexpr int64_t kMaxB128N = (int64_t)1 << 24;
 constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;   // 128 x 128, of one call to quantize: 550 GB
 constexpr int64_t kMaxIndexedBytes = 0xffe00000;   // what a buffer resource covers
 constexpr int64_t kMaxOutputs = (int64_t)1 << 38;   // of one product: 512 GB, past the card's memory
 
@@ -99,6 +100,8 @@ llmint8_status_t llmint8_quantize_weight_b128(const uint16_t *W_t, int type, int
     const llmint8_status_t st = check_b128(1, K, N, E);
     if (st != LLMINT8_OK)
         return st;
+    if (E * ((N + kB128 - 1) / kB128) * ((K + kB128 - 1) / kB128) > kMaxBlocks)
+        return LLMINT8_ERR_UNSUPPORTED_SHAPE;
     return status(launch_quantize_weight_b128(W_t, E, N, K, type, CB8, SB, stream));
 }
 

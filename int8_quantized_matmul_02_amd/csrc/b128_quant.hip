@@ -381,8 +381,6 @@ hipError_t launch_quantize_weight_b128(const uint16_t *W, int64_t E, int64_t N, 
                                        int type, uint8_t *CB, uint8_t *SB, hipStream_t s)
 {
     const int64_t nb = (N + kB128 - 1) / kB128, kbs = (K + kB128 - 1) / kB128;
-    if (E * nb * kbs >= (int64_t)1 << 24)   // 550 GB of weights
-        return hipErrorInvalidValue;
     const dim3 grid((unsigned)(E * nb * kbs));
     const int pitch = (int)b128_pitch(K);
     if (type == kTypeBf16)

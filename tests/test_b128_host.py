@@ -59,7 +59,8 @@ def test_quantizer_refusals(lib):
                dict(S=P + 2), dict(ty=3), dict(E=0), dict(N=0), dict(K=0)):
         assert w(**kw) == 1, kw
     assert a(K=72) == 2 and a(K=133184) == 2
-    for kw in (dict(K=96), dict(N=96), dict(K=133184), dict(N=(1 << 24) + 64), dict(E=1025)):
+    for kw in (dict(K=96), dict(N=96), dict(K=133184), dict(N=(1 << 24) + 64), dict(E=1025),
+               dict(E=1024, N=1 << 21, K=64)):
         assert w(**kw) == 2, kw
 
 

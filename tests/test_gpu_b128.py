@@ -587,3 +587,104 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in (0, 1):
         assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+def codes(shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(0, 0x78, shape, dtype=torch.uint8, device="cuda", generator=g)
+
+
+def scales(shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(110, 116, shape, dtype=torch.uint8, device="cuda", generator=g)
+
+
+BIG_T = (1 << 26) + 300    # rows of 64: more than 2^32 elements
+
+
+def test_large_activations():
+    """Rows whose bytes, and output bytes, lie past 2^32, against calls on a copy of those rows."""
+    T, K, N = BIG_T, 64, 64
+    q, s = codes((T, K), 1), scales((T, 4), 2)
+    w, b = codes((N, K), 3), scales((1, 4), 4)
+    rows = [slice(0, 300), slice((1 << 25) - 150, (1 << 25) + 150),
+            slice((1 << 26) - 150, (1 << 26) + 150), slice(T - 300, T)]
+    for path in (0, 4, 6, 7, 8, 9):
+        say("large activations", path)
+        out = L.llmint8.llmint8_matmul_b128_path(q, s, w, b, path=path, parts=1)
+        for r in rows:
+            part = L.llmint8.llmint8_matmul_b128_path(q[r].clone(), s[r].clone(), w, b, path=path,
+                                                      parts=1)
+            assert torch.equal(out[r], part), (path, r)
+        del out
+
+
+def test_large_activations_by_index():
+    """The largest matrix that rows may be read from by index."""
+    T, K, N, M = 0xffe00000 // 64, 64, 64, 700
+    q, s = codes((T, K), 1), scales((T, 4), 2)
+    w, b = codes((3, N, K), 3), scales((3, 1, 4), 4)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    idx = torch.randint(T - (1 << 20), T, (M,), dtype=torch.int32, device="cuda", generator=g)
+    idx[:4] = torch.tensor([T - 1, 0, 1 << 25, T - 2], dtype=torch.int32)
+    off = torch.tensor([0, 300, 301, M], dtype=torch.int32, device="cuda")
+    for path in (0, 1, 6, 7, 8, 9):
+        say("large, by index", path)
+        f = L.llmint8.llmint8_matmul_grouped_b128_path
+        assert torch.equal(f(q, s, w, b, off, row_idx=idx, path=path),
+                           f(q[idx.long()], s[idx.long()], w, b, off, path=path)), path
+
+
+def test_large_weights():
+    """Weights past 2^32 bytes, one matrix or the last of a stack of experts."""
+    K, N, E = 4160, (1 << 20) + 1024, 16
+    w, b = codes((N, K), 1), scales((N // 128, 36), 2)
+    be = scales((E, (N // E + 127) // 128, 36), 3)
+    for T, paths in ((5, (0, 1, 4)), (300, (0, 6, 7, 8, 9))):
+        q, s = codes((T, K), T), scales((T, 36), T + 1)
+        off = torch.tensor([0] * (E - 1) + [T // 2, T], dtype=torch.int32, device="cuda")
+        for path in paths:
+            say("large weights", T, path)
+            out = L.llmint8.llmint8_matmul_b128_path(q, s, w, b, path=path, parts=1)
+            p = path or int(T > 16) * 8 + 1     # any fixed tile
+            part = L.llmint8.llmint8_matmul_b128_path(q, s, w[-512:], b[-4:], path=p, parts=1)
+            if path:
+                assert torch.equal(out[:, -512:], part), path
+            else:
+                # positive sums in another order, rounded to fp16: one step at most
+                torch.testing.assert_close(out[:, -512:], part, rtol=2.0 ** -9, atol=0)
+            f = L.llmint8.llmint8_matmul_grouped_b128_path
+            if path:
+                got = f(q, s, w.view(E, N // E, K), be, off, path=path)
+                last = f(q, s, w.view(E, N // E, K)[-2:], be[-2:], off[-3:], path=path)
+                assert torch.equal(got, last), path
+
+
+def test_large_quantizers():
+    """More than 2^32 elements, against calls on a copy of the last rows."""
+    T, K = BIG_T, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.empty((T, K), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    gamma = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    say("large act")
+    q, s = L.llmint8_quantize_act_b128(X)
+    say("large norm")
+    n, ns, h = L.llmint8_rmsnorm_b128(X, gamma, residual=X)
+    say("large weight")
+    c, cs = L.llmint8_quantize_weight_b128(X[:1 << 26].view(4, 1 << 24, K))
+    c, cs = c.view(-1, K), cs.view(-1, 4)
+    for r in (slice(0, 512), slice((1 << 25) - 256, (1 << 25) + 256),
+              slice((1 << 26) - 256, (1 << 26))):
+        x = X[r].clone()
+        for a, b in zip(L.llmint8_quantize_act_b128(x), (q, s)):
+            assert torch.equal(a, b[r])
+        for a, b in zip(L.llmint8_rmsnorm_b128(x, gamma, residual=x), (n, ns, h)):
+            assert torch.equal(a, b[r])
+        a, b = L.llmint8_quantize_weight_b128(x)
+        assert torch.equal(a, c[r]) and torch.equal(b, cs[r.start // 128:r.stop // 128])
+    r = slice(T - 300, T)
+    for a, b in zip(L.llmint8_quantize_act_b128(X[r].clone()), (q, s)):
+        assert torch.equal(a, b[r])
+    x = X[r].clone()
+    for a, b in zip(L.llmint8_rmsnorm_b128(x, gamma, residual=x), (n, ns, h)):
+        assert torch.equal(a, b[r])
