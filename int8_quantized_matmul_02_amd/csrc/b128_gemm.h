@@ -24,6 +24,8 @@
 //    over the wavefronts of a block (few rows: bound by reading the weight).
 #pragma once
 
+#include <utility>
+
 #include "b128.h"
 #include "gemm_kernel.h"
 
@@ -521,6 +523,18 @@ struct BigCfg {
 // against 214 at 4096 x 4096 x 16384).
 __device__ __forceinline__ void pin(v4f &v) { asm volatile("" : "+a"(v)); }
 
+// f(0), ..., f(N - 1), each with its index as a constant.
+template <int... M, class F>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, M...>, F f)
+{
+    (f(std::integral_constant<int, M>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each_index(F f)
+{
+    each_of(std::make_integer_sequence<int, N>(), f);
+}
+
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 
 // The stage loads of a block, running ahead of its products.  Scalar offsets
@@ -723,15 +737,12 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
         lds_load4(rsw, (lds_void *)(sc + C::kScaleRows + wave * 256), lane % 4 * 4,
                   (uint32_t)(t.k0 + c * C::kChunk));
     };
-    int sx[C::FM], sw;   // the MFMA reads the low byte
-    auto read_scales = [&](int kt) {
-        const int8_t *sc = reinterpret_cast<const int8_t *>(smem) + C::kRing +
-                            (kt / C::kChunk & 1) * C::kScaleBytes + kt % C::kChunk;
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-            sx[i] = sc[(wm * C::kTM + i * 16 + r) * C::kChunk];
-        sw = sc[C::kScaleRows + wave * 256];
+    unsigned sx[C::FM], sw, next_sw;   // the MFMA reads the low byte
+    auto scales_at = [&](int kt) {
+        return reinterpret_cast<const uint8_t *>(smem) + C::kRing +
+               (kt / C::kChunk & 1) * C::kScaleBytes + kt % C::kChunk;
     };
+    const int sxoff = (wm * C::kTM + r) * C::kChunk, swoff = C::kScaleRows + wave * 256;
 
     Loader<C, kGather> ld;
     auto load_stage = [&](int s) {
@@ -790,54 +801,71 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
         else
             wait_vm<(C::STAGES - 1) * C::kLoads + C::kStores>();
         __builtin_amdgcn_s_barrier();
-        read_scales(0);
+        sw = scales_at(0)[swoff];
+        asm volatile("" : "+v"(sw));
 #pragma unroll
-        for (int i = 0; i < C::FM - 2; ++i)
+        for (int i = 0; i < C::FM - 2; ++i) {
+            sx[i] = scales_at(0)[sxoff + i * 16 * C::kChunk];
             read_a(smem, i);
+        }
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
             read_b(smem, j);
+#pragma unroll
+        for (int i = 0; i < C::FM - 2; ++i) {
+            asm volatile("" : "+v"(sx[i]));
+            asm volatile("" : "+v"(fa[i]));
+        }
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+            asm volatile("" : "+v"(fb[j]));
         for (int kt = 0; kt < t.nk; ++kt) {
             const char *cbuf = smem + kt % C::STAGES * C::kStageBytes;
             const char *nbuf = smem + (kt + 1) % C::STAGES * C::kStageBytes;
+            const uint8_t *cs = scales_at(kt), *ns = scales_at(kt + 1);
             const StageLoad<C, kGather> sl(ld, smem, t, kt + C::STAGES, half);
             // the other chunk's last bytes were read before the last barrier
             if (kt % C::kChunk == 0 && kt + C::kChunk < t.nk)
                 load_scales(kt / C::kChunk + 1);
-#pragma unroll
-            for (int m = 0; m < C::kMfmas; ++m) {
-                const int p = m / C::kPair, w = m % C::kPair;   // pair, place in it
-                const int i = 2 * p + w % 2, j = w / 2;
-                if (m == 0)
-                    read_a(cbuf, C::FM - 2);
-                if (m == 2)
-                    read_a(cbuf, C::FM - 1);
-                if (m == C::kFree) {   // every wavefront has read all of this stage
+            each_index<C::kMfmas>([&](auto index) __attribute__((always_inline)) {
+                constexpr int m = decltype(index)::value;
+                constexpr int p = m / C::kPair, w = m % C::kPair;   // pair, place in it
+                constexpr int i = 2 * p + w % 2, j = w / 2;
+                if constexpr (m == 0 || m == 2) {
+                    constexpr int l = C::FM - 2 + m / 2;
+                    read_a(cbuf, l);
+                    sx[l] = cs[sxoff + l * 16 * C::kChunk];
+                }
+                if constexpr (m == C::kFree) {   // every wavefront has read all of this stage
                     gemm::wait_lds();
                     __builtin_amdgcn_s_barrier();
                 }
-                if (m == C::kLand) {   // the next stage has landed for every wavefront
+                if constexpr (m == C::kLand) {   // the next stage has landed for every wavefront
                     wait_vm<(C::STAGES - 2) * C::kLoads + C::before(C::kLand)>();
                     __builtin_amdgcn_s_barrier();
                 }
+                if constexpr (p > 0 && w < 2)   // the pair before has taken its scales
+                    sx[i - 2] = ns[sxoff + (i - 2) * 16 * C::kChunk];
+                if constexpr (m == C::kPair + 2)
+                    next_sw = ns[swoff];
 #pragma unroll
                 for (int u = C::before(m); u < C::before(m + 1); ++u)
                     sl.issue(ld, wave, u);
-                if (m >= C::kLand && (m - C::kLand) % 2 == 0 &&
-                    (m - C::kLand) / 2 < 2 * (C::kPairs - 2))
+                if constexpr (m >= C::kLand && (m - C::kLand) % 2 == 0 &&
+                              (m - C::kLand) / 2 < 2 * (C::kPairs - 2))
                     read_a(nbuf, (m - C::kLand) / 2);
-                if (p == C::kPairs - 1 && (w == 0 || w == 2))
+                if constexpr (p == C::kPairs - 1 && (w == 0 || w == 2))
                     read_a(nbuf, C::FM - 4 + w / 2);
-                if (p == C::kPairs - 1 && w >= 2 && w % 2 == 0)
+                if constexpr (p == C::kPairs - 1 && w >= 2 && w % 2 == 0)
                     read_b(nbuf, j - 1);
                 pin(acc[i][j]);
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                     fb[j], fa[i], acc[i][j], 0, 0, 0, sw, 0, sx[i]);
                 pin(acc[i][j]);
                 __builtin_amdgcn_sched_barrier(0);
-            }
+            });
             read_b(nbuf, C::FN - 1);
-            read_scales(kt + 1);
+            sw = next_sw;
         }
         const Tile done = t;
         v += gridDim.x;
