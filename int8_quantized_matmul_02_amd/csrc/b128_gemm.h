@@ -445,16 +445,17 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
 // 4096 x 16384 x 4096 and 8192^3: a load per MFMA 227, 231, 428 us; before every
 // 2nd 216, 209, 405; every 3rd 214, 197, 400.
 //
-// What bounds it: a stage of 256 x 256 takes 2850 cycles on a compute unit, 2048
-// of them MFMAs (64 of 32 cycles per SIMD), 600 waiting at the two barriers.  With
-// all compute units busy the power limit then holds the clock at 1.8 - 2.0 GHz
-// (alone, a tile runs at 2.37): 4096 x 4096 x 16384 in 214 us = 2570 TFLOP/s,
-// where the library's product of per-tensor scales takes 219; 8192^3 400 us (395).
-// A stage of 128 x 128 takes 1110 cycles against 512 of MFMAs, the transfers into
-// and out of LDS 768; two resident blocks share them.  Deeper rings (128 x 128
-// with 4 stages, 64 x 128 with 6) change nothing there.  Experts' weights come
-// cold, in pieces of 128 bytes a row apart, at up to 4.4 TB/s (pieces of 512: 5.1):
-// 8 x 4096 x 4096 with 64 rows each 38 us = 3.5 TB/s.
+// What bounds it: alone on the card a tile of 256 x 256 takes 2475 cycles per
+// stage at 2.37 GHz, 2048 of them MFMAs (64 of 32 cycles per SIMD); of the rest the
+// fragments' reads take 120, the scales' 60, barriers and loads 250.  With all
+// compute units busy the power limit holds the clock at 1.8 - 2.0 GHz: 4096 x 4096
+// x 16384 in 216 us = 2550 TFLOP/s, where the library's product of per-tensor scales
+// takes 227 on the same card; 8192^3 401 us (404).  A stage of 128 x 128 takes 960
+// cycles alone against 512 of MFMAs; two on each of all compute units take 0.95 us,
+// 0.25 of it for their loads (17 TB/s from L2).  Deeper rings (128 x 128 with 4
+// stages, 64 x 128 with 6) change nothing there.  Experts' weights come cold, in
+// pieces of 128 bytes a row apart, at up to 4.4 TB/s (pieces of 512: 5.1): 8 x 4096
+// x 4096 with 64 rows each 38 us = 3.5 TB/s.
 //
 // Blocks are persistent: a block takes tiles v, v + grid, ..., and loads the
 // next tile's first stages before it writes a finished tile out.  Past a
@@ -467,7 +468,10 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
 // both operands.  A last block of 64 columns is staged with zeros for chunks
 // 4 .. 7 (their lanes' offsets lie outside the resource).  The scales of 16
 // stages (16 bytes of each row) are loaded into LDS together, a chunk ahead,
-// in two buffers, and read a byte per row tile and stage.  (Loads of scales
+// in two buffers, and read a byte per row tile and stage, as soon as the stage's
+// products have taken the one before (read at the stage's end instead, they hold
+// the next stage's first product back: 1.163 against 1.121 us per block of K of one
+// tile of 256 x 256, 220 against 216 us at 4096 x 4096 x 16384).  (Loads of scales
 // into registers made the compiler wait for all loads in flight once per
 // stage.)
 // ---------------------------------------------------------------------------
@@ -811,6 +815,8 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_big(B128Args a)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
             read_b(smem, j);
+        // Used here, so that they are waited for here: the loop's first products
+        // then wait for what its own iterations read only.
 #pragma unroll
         for (int i = 0; i < C::FM - 2; ++i) {
             asm volatile("" : "+v"(sx[i]));
