@@ -590,8 +590,8 @@ def llmint8_matmul_e4m3(X, CB8, SC8, threshold=6.0, bias=None, out=None, ws=None
 # 16-bit tensors are float16 or bfloat16, all of one call of one dtype.
 #
 # A decoded token's calls take a few microseconds on the GPU, so the checks
-# here are one pass of attribute comparisons (_ok); only a call that fails one
-# goes through _arg and _on_device, for their message.
+# here are one pass of attribute comparisons (_ok, and _ready for the products);
+# only a call that fails one goes through _arg and _on_device, for their message.
 # ---------------------------------------------------------------------------
 _TYPES = {torch.float16: 0, torch.bfloat16: 1}
 _T16 = (torch.float16, torch.bfloat16)
@@ -599,7 +599,7 @@ _CODES = (torch.uint8, torch.float8_e4m3fn)
 _SCALES = (torch.uint8, torch.float8_e8m0fnu)
 _U8 = torch.uint8
 _empty_like, _empty_strided = torch.empty_like, torch.empty_strided
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream   # its handle, by device index
 
 
@@ -655,6 +655,30 @@ def llmint8_rmsnorm_b128(X, gamma, eps=1e-6, residual=None, residual_out=None, Y
     normalized rows and the sum X + residual, which is allocated if there is a residual
     and none is given (pass `residual` itself to update it in place).  Y: a tensor
     [T,K] that also receives the normalized rows in X's dtype."""
+    if residual_out is None and Xq8 is None and SX is None:
+        try:
+            dev, dt, shape = X.get_device(), X.dtype, X.shape
+            T, K = shape
+            if (T and dt in _T16 and 0 <= dev == _current_device() == gamma.get_device()
+                    and gamma.dtype == dt and gamma.shape == (K,) and X.is_contiguous()
+                    and gamma.is_contiguous()
+                    and (residual is None or residual.get_device() == dev
+                         and residual.dtype == dt and residual.shape == shape
+                         and residual.is_contiguous())
+                    and (Y is None or Y.get_device() == dev and Y.dtype == dt
+                         and Y.shape == shape and Y.is_contiguous())):
+                h = None if residual is None else _empty_like(X)
+                q, sx = _empty_like(X, dtype=_U8), _matrix(T, (K + 511) // 512 * 4, _U8, X.device)
+                rc = (_lib or _load()).llmint8_rmsnorm_b128(
+                    X.data_ptr(), None if residual is None else residual.data_ptr(),
+                    gamma.data_ptr(), _TYPES[dt], T, K, eps, q.data_ptr(), sx.data_ptr(),
+                    None if h is None else h.data_ptr(), None if Y is None else Y.data_ptr(),
+                    _current_stream(dev))
+                if rc != LLMINT8_OK:
+                    raise LLMInt8Error("llmint8_rmsnorm_b128", rc)
+                return q, sx, h
+        except (AttributeError, TypeError, ValueError):
+            pass   # checked one by one below
     shape = _sizes(X, "X", _T16, 2)
     T, K = shape
     dev, dt = X.get_device(), (X.dtype,)
@@ -690,6 +714,20 @@ def llmint8_rmsnorm_b128(X, gamma, eps=1e-6, residual=None, residual_out=None, Y
 def llmint8_quantize_act_b128(X, Xq8=None, SX=None):
     """X: fp16 or bf16 [T,K].  Returns (Xq8 uint8 [T,K] E4M3 codes, SX uint8 [T,pitch] scales of
     its 1 x 128 blocks)."""
+    if Xq8 is None and SX is None:
+        try:
+            dev, dt = X.get_device(), X.dtype
+            T, K = X.shape
+            if T and dt in _T16 and 0 <= dev == _current_device() and X.is_contiguous():
+                q, sx = _empty_like(X, dtype=_U8), _matrix(T, (K + 511) // 512 * 4, _U8, X.device)
+                rc = (_lib or _load()).llmint8_quantize_act_b128(
+                    X.data_ptr(), _TYPES[dt], T, K, q.data_ptr(), sx.data_ptr(),
+                    _current_stream(dev))
+                if rc != LLMINT8_OK:
+                    raise LLMInt8Error("llmint8_quantize_act_b128", rc)
+                return q, sx
+        except (AttributeError, TypeError, ValueError):
+            pass   # checked one by one below
     shape = _sizes(X, "X", _T16, 2)
     T, K = shape
     dev = X.get_device()
@@ -726,6 +764,22 @@ def llmint8_quantize_weight_b128(W_t, CB8=None, SB=None):
     _launch("llmint8_quantize_weight_b128", W_t.get_device(), W_t.data_ptr(), _TYPES[W_t.dtype], E,
             K, N, CB8.data_ptr(), SB.data_ptr())
     return CB8, SB
+
+
+def _ready(Xq8, SX, CB8, SB, bias, out, dt, sx, sb, b, o):
+    """The device index of a product's operands if they, and bias and out if given, are all that
+    they have to be (sx, sb, b, o: the shapes of SX, SB, bias, out), else -1."""
+    dev = Xq8.get_device()
+    if (dev == SX.get_device() == CB8.get_device() == SB.get_device() and Xq8.dtype in _CODES
+            and CB8.dtype in _CODES and SX.dtype in _SCALES and SB.dtype in _SCALES
+            and SX.shape == sx and SB.shape == sb and Xq8.is_contiguous() and SX.is_contiguous()
+            and CB8.is_contiguous() and SB.is_contiguous() and dt in _TYPES
+            and (bias is None or bias.get_device() == dev and bias.dtype == dt and bias.shape == b
+                 and bias.is_contiguous())
+            and (out is None or out.get_device() == dev and out.dtype == dt and out.shape == o
+                 and out.is_contiguous())):
+        return dev
+    return -1
 
 
 def _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, lead, offsets, row_idx, ws):
@@ -799,6 +853,32 @@ def llmint8_matmul_b128(Xq8, SX, CB8, SB, bias=None, activation=ACT_NONE, out=No
     llmint8_quantize_weight_b128) -> out [T,N] in out_dtype (out's own dtype if given;
     bias [N] has the same).  ws: at least llmint8_matmul_b128_workspace_bytes(T, K, N)
     bytes, allocated if needed and not given."""
+    dev = -1
+    if ws is None:
+        try:
+            T, K = Xq8.shape
+            N, k = CB8.shape
+            p = (K + 511) // 512 * 4
+            dt = out_dtype if out is None else out.dtype
+            if T and K == k:
+                dev = _ready(Xq8, SX, CB8, SB, bias, out, dt, (T, p), ((N + 127) // 128, p), (N,),
+                             (T, N))
+        except (AttributeError, TypeError, ValueError):
+            pass
+    if dev >= 0 and _current_device() == dev:
+        need = _b128_need(T, K, N, 0, 0)
+        if need:
+            ws = torch.empty((need,), dtype=_U8, device=Xq8.device)
+        if out is None:
+            out = _empty_strided((T, N), (N, 1), dtype=dt, device=Xq8.device)
+        rc = (_lib or _load()).llmint8_matmul_b128(
+            Xq8.data_ptr(), SX.data_ptr(), T, K, N, CB8.data_ptr(), SB.data_ptr(),
+            None if bias is None else bias.data_ptr(), activation, _TYPES[dt], out.data_ptr(),
+            ws.data_ptr() if need else None, need, _current_stream(dev))
+        if rc != LLMINT8_OK:
+            raise LLMInt8Error("llmint8_matmul_b128", rc)
+        return out
+    # anything else is checked one by one
     return llmint8_matmul_b128_path(Xq8, SX, CB8, SB, bias, activation, out, out_dtype, ws)
 
 
@@ -827,5 +907,34 @@ def llmint8_matmul_grouped_b128(Xq8, SX, CB8, SB, offsets, row_idx=None, bias=No
     device; row_idx int32 [M] on the device: output row i reads row row_idx[i] of Xq8 (row i
     without it).  Returns out [M,N]; rows outside [offsets[0], offsets[E]) are left as they were.
     M = 0 returns the empty output."""
+    dev = -1
+    try:
+        T, K = Xq8.shape
+        E, N, k = CB8.shape
+        M = T if row_idx is None else row_idx.shape[0]
+        p = (K + 511) // 512 * 4
+        dt = out_dtype if out is None else out.dtype
+        if (M and K == k and offsets.dtype == torch.int32 and offsets.shape == (E + 1,)
+                and offsets.is_contiguous()
+                and (row_idx is None or row_idx.dtype == torch.int32 and row_idx.dim() == 1
+                     and row_idx.is_contiguous())):
+            dev = _ready(Xq8, SX, CB8, SB, bias, out, dt, (T, p), (E, (N + 127) // 128, p), (E, N),
+                         (M, N))
+            if offsets.get_device() != dev or row_idx is not None and row_idx.get_device() != dev:
+                dev = -1
+    except (AttributeError, TypeError, ValueError, IndexError):
+        pass
+    if dev >= 0 and _current_device() == dev:
+        if out is None:
+            out = _empty_strided((M, N), (N, 1), dtype=dt, device=Xq8.device)
+        rc = (_lib or _load()).llmint8_matmul_grouped_b128(
+            Xq8.data_ptr(), SX.data_ptr(), T, K, N, CB8.data_ptr(), SB.data_ptr(), E,
+            offsets.data_ptr(), None if row_idx is None else row_idx.data_ptr(), M,
+            None if bias is None else bias.data_ptr(), activation, _TYPES[dt], out.data_ptr(),
+            _current_stream(dev))
+        if rc != LLMINT8_OK:
+            raise LLMInt8Error("llmint8_matmul_grouped_b128", rc)
+        return out
+    # anything else is checked one by one
     return llmint8_matmul_grouped_b128_path(Xq8, SX, CB8, SB, offsets, row_idx, bias, activation,
                                             out, out_dtype)

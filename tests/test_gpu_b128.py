@@ -688,3 +688,45 @@ def test_large_quantizers():
     x = X[r].clone()
     for a, b in zip(L.llmint8_rmsnorm_b128(x, gamma, residual=x), (n, ns, h)):
         assert torch.equal(a, b[r])
+
+
+def spoiled(t):
+    """Copies of a tensor that no call may take in its place."""
+    yield "on the host", t.cpu()
+    yield "of another type", t.to(torch.float64)
+    yield "of another shape", torch.cat([t, t])
+    yield "of another rank", t[None]
+    if t.dim() > 1 and t.shape[-2] > 1:    # (a single row is contiguous either way)
+        yield "not contiguous", t.transpose(-1, -2).contiguous().transpose(-1, -2)
+
+
+def test_refusals_of_device_tensors():
+    """Every tensor argument, on the host, of another type, shape or layout, is refused."""
+    d, T, K, N, E, M = dev(), 6, 192, 128, 3, 5
+    xq, sx, wq, sw = up(*operands(T, K, N, 1, E=E))
+    h = torch.float16
+    off = torch.tensor([0, 2, 2, M], dtype=torch.int32, device=d)
+    idx = torch.zeros(M, dtype=torch.int32, device=d)
+    z = lambda *n: torch.zeros(n, dtype=h, device=d)  # noqa: E731
+    calls = [
+        (L.llmint8_rmsnorm_b128, dict(X=z(T, K), gamma=z(K), residual=z(T, K), Y=z(T, K))),
+        (L.llmint8_rmsnorm_b128, dict(X=z(T, K), gamma=z(K), residual=z(T, K),
+                                      residual_out=z(T, K), Xq8=torch.empty_like(xq),
+                                      SX=torch.empty_like(sx))),
+        (L.llmint8_quantize_act_b128, dict(X=z(T, K), Xq8=torch.empty_like(xq))),
+        (L.llmint8_quantize_weight_b128, dict(W_t=z(N, K), CB8=torch.empty_like(wq[0]))),
+        (L.llmint8_matmul_b128, dict(Xq8=xq, SX=sx, CB8=wq[0], SB=sw[0], bias=z(N), out=z(T, N))),
+        (L.llmint8_matmul_grouped_b128, dict(Xq8=xq, SX=sx, CB8=wq, SB=sw, offsets=off,
+                                             row_idx=idx, bias=z(E, N), out=z(M, N))),
+    ]
+    for f, args in calls:
+        f(**args)
+        for name in args:
+            for what, bad in spoiled(args[name]):
+                with pytest.raises((TypeError, ValueError)):
+                    f(**{**args, name: bad})
+                    pytest.fail("%s took %s %s" % (f.__name__, name, what))
+    with pytest.raises((TypeError, ValueError)):
+        L.llmint8_matmul_b128(xq, sx, wq[0], sw[0], bias=z(N), out_dtype=torch.bfloat16)
+    with pytest.raises((TypeError, ValueError)):
+        L.llmint8_matmul_b128(xq.cpu().numpy(), sx, wq[0], sw[0])
