@@ -103,11 +103,11 @@ LLMINT8_API llmint8_status_t llmint8_mfma_ceiling(const void *A, int64_t T, cons
 
 /*
  * llmint8_matmul_b128 and llmint8_matmul_grouped_b128 with the kernel chosen:
- * path 1 .. 9 forces a tile of 16 x 16, 16 x 32 (three stages in flight), 16 x 32
- * (two), 16 x 64, 32 x 64, 64 x 64, 64 x 128, 128 x 128 or 256 x 256 outputs, 0 leaves
- * the choice; parts 1 .. 8 forces into how many
- * parts K is split (fewer if it has fewer groups of 512 columns), 0 leaves the
- * choice.  Others -> LLMINT8_ERR_INVALID_ARG.
+ * path 1 .. 10 forces a tile of 16 x 16, 16 x 32 (three stages in flight), 16 x 32
+ * (two), 16 x 64, 32 x 64, 64 x 64, 64 x 128, 128 x 128, 256 x 256 or 256 x 128
+ * outputs, 0 leaves the choice; parts 1 .. 8 forces into how many parts K is split
+ * (fewer if it has fewer groups of 512 columns), 0 leaves the choice.  Others ->
+ * LLMINT8_ERR_INVALID_ARG.
  */
 LLMINT8_API size_t llmint8_matmul_b128_workspace_bytes_path(int64_t T, int64_t K, int64_t N,
                                                             int path, int parts);

@@ -118,7 +118,7 @@ struct B128Args {
 };
 // path: 0, or one of the kernel shapes 1 .. kB128Paths; parts: 0, or into how
 // many parts K is split (1 for a grouped product); both 0: the estimate's choice.
-constexpr int kB128Paths = 9, kB128MostParts = 8;
+constexpr int kB128Paths = 10, kB128MostParts = 8;
 hipError_t launch_matmul_b128(const B128Args &a, void *ws, int path, int parts, hipStream_t s);
 size_t b128_workspace_bytes(int64_t T, int64_t K, int64_t N, int path, int parts);
 

@@ -497,7 +497,11 @@ struct BigCfg {
     // the stage's schedule, in MFMAs
     static constexpr int kMfmas = FM * FN, kPair = 2 * FN, kPairs = FM / 2;
     static constexpr int kFree = kMfmas >= 64 ? 6 : kMfmas >= 16 ? 4 : 3;
-    static constexpr int kLand = kPairs > 2 ? kMfmas * 5 / 8 : kMfmas / 2;
+    // what is read of A before the last pair takes two MFMAs a tile
+    static constexpr int kLatest = (kPairs - 1) * kPair - 4 * (kPairs - 2);
+    static constexpr int kLand = kPairs <= 2               ? kMfmas / 2
+                                 : kMfmas * 5 / 8 < kLatest ? kMfmas * 5 / 8
+                                                            : kLatest;
     static constexpr int slot(int load)   // the MFMA before which a stage load is issued
     {
         const int room = kMfmas - kFree, step = room / kLoads;

@@ -14,13 +14,14 @@ using Small32x64 = b128::SmallCfg<32, 64, 1, 2, 4, 3>;
 using Small64x64 = b128::SmallCfg<64, 64, 2, 2, 2, 2>;
 using Big64x128 = b128::BigCfg<64, 128, 1, 4, 3, 4>;
 using Big128 = b128::BigCfg<128, 128, 2, 2, 2, 4>;
+using Big256x128 = b128::BigCfg<256, 128, 2, 2, 2, 4>;
 using Big256 = b128::BigCfg<256, 256, 2, 2, 2, 4>;
 
 namespace {
 
 // The tile and the parts of K are those with the least estimated time.  In
-// microseconds, with constants fitted to sweeps over 630 plain and grouped
-// sizes on MI355X, each with all shapes that could matter and 1, 2, 4 or 8 parts:
+// microseconds, with constants fitted to sweeps over 1000 plain and grouped sizes
+// on MI355X, each with all shapes that could matter and 1, 2, 4 or 8 parts:
 //   * a block reads (BM + BN) * K bytes at what its compute unit draws: the
 //     bytes its resident blocks keep in flight over 0.5 us of latency, at most
 //     68 KB/us;
@@ -29,12 +30,14 @@ namespace {
 //   * the weight, read from HBM rather than L2, adds its bytes at 12 TB/s;
 //   * a split of K adds a launch and its partial sums, written and read;
 //   * an expert's last tile, on average, wastes 0.6 of its rows.
-// The choice takes 1.3 % longer than the best of them (geometric mean; grouped
-// 1.6 %, whose row counts the host does not know).  Some of the sweep, in us:
+// The choice takes 1.4 % longer than the best of them (geometric mean; grouped
+// 1.9 %, whose row counts the host does not know).  Some of the sweep, in us:
 // 1 x 4096 x 16384: 16 x 32 13.9, 16 x 16 15.6; 1 x 16384 x 4096: 16 x 16 14.2, 16 x 32
 // 16.1; 300 x 2048 x 8192: 128 x 128 12.8, 64 x 128 15.2; 256 x 16384 x 4096: 128 x 128
-// in 4 parts 36.5, 64 x 64 whole 42.8; 4096 x 4096 x 16384: 256 x 256 209, 128 x 128 277;
-// 2222 rows of 8 experts, K = N = 4096: 256 x 256 58, 128 x 128 71.
+// in 4 parts 36.5, 64 x 64 whole 42.8; 512 x 4096 x 16384: 256 x 128 38.0, 128 x 128
+// 42.1; 4096 x 4096 x 16384: 256 x 256 209, 128 x 128 277; 2222 rows of 8 experts, K =
+// N = 4096: 256 x 256 58, 128 x 128 71; 2048 rows, 256 each: 256 x 128 46.4, 128 x 128
+// 53.4, 256 x 256 55.6.
 struct Shape {
     int bm, bn;
     int resident;         // blocks per compute unit
@@ -60,6 +63,7 @@ const Shape kShapes[kB128Paths] = {
     small_shape<Small16x16>(),   small_shape<Small16x32>(), small_shape<Small16x32s2>(),
     small_shape<Small16x64>(),   small_shape<Small32x64>(), small_shape<Small64x64>(),
     big_shape<Big64x128>(5.2, 0.0), big_shape<Big128>(5.2, 0.0), big_shape<Big256>(11.4, 1.15),
+    big_shape<Big256x128>(9.6, 0.0),
 };
 constexpr double kLatency = 0.5, kCuRate = 68e3, kWeightRate = 12e6, kSumRate = 5.3e6;   // us, bytes per us
 constexpr int kCUs = 256;

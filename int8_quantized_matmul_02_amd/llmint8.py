@@ -830,7 +830,7 @@ def llmint8_matmul_b128_workspace_bytes(T, K, N, path=0, parts=0):
 
 def llmint8_matmul_b128_path(Xq8, SX, CB8, SB, bias=None, activation=ACT_NONE, out=None,
                              out_dtype=torch.float16, ws=None, path=0, parts=0):
-    """llmint8_matmul_b128 with the kernel's tile (path 1 .. 9) and the number of parts of K
+    """llmint8_matmul_b128 with the kernel's tile (path 1 .. 10) and the number of parts of K
     chosen; 0 leaves the choice to the library."""
     T, K, N, _, dev, out = _b128_operands(Xq8, SX, CB8, SB, bias, out, out_dtype, (), None, None,
                                           ws)
@@ -885,7 +885,7 @@ def llmint8_matmul_b128(Xq8, SX, CB8, SB, bias=None, activation=ACT_NONE, out=No
 def llmint8_matmul_grouped_b128_path(Xq8, SX, CB8, SB, offsets, row_idx=None, bias=None,
                                      activation=ACT_NONE, out=None, out_dtype=torch.float16,
                                      path=0):
-    """llmint8_matmul_grouped_b128 with the kernel's tile chosen (path 1 .. 9; 0: the library's
+    """llmint8_matmul_grouped_b128 with the kernel's tile chosen (path 1 .. 10; 0: the library's
     choice)."""
     if not isinstance(CB8, torch.Tensor) or CB8.dim() != 3:
         raise ValueError("CB8 must be a tensor [E,N,K]")

@@ -262,7 +262,7 @@ def test_matmul(K, N, exact):
         assert (out[T:] == 9.0).all(), "rows behind the output"
 
 
-@pytest.mark.parametrize("path", range(1, 10))
+@pytest.mark.parametrize("path", range(1, 11))
 @pytest.mark.parametrize("T,K,N", [(1, 64, 64), (70, 320, 192), (300, 1088, 576), (257, 2304, 320),
                                    (530, 4160, 448)])
 def test_matmul_every_tile(T, K, N, path):
@@ -286,7 +286,8 @@ def test_matmul_every_tile(T, K, N, path):
 
 
 @pytest.mark.parametrize("path,T,K,N", [(9, 8100, 320, 4160), (8, 3000, 192, 5056),
-                                        (7, 4100, 576, 2112), (9, 4096, 1024, 4096)])
+                                        (7, 4100, 576, 2112), (9, 4096, 1024, 4096),
+                                        (10, 5000, 448, 4160)])
 def test_matmul_many_tiles(path, T, K, N):
     """More tiles than a launch has blocks: each block takes several."""
     say("many tiles", T, K, N, path)
@@ -367,7 +368,7 @@ def test_grouped(K, N, exact):
         assert (out[:first] == 9.0).all() and (out[off[-1]:] == 9.0).all(), "rows of no group"
 
 
-@pytest.mark.parametrize("path", range(1, 10))
+@pytest.mark.parametrize("path", range(1, 11))
 def test_grouped_every_tile(path):
     d = dev()
     for rows, K, N, gather in (([70, 0, 129, 2], 320, 192, True), ([300, 5, 0, 31, 64], 192, 320, False),
@@ -391,7 +392,7 @@ def test_grouped_every_tile(path):
         assert (out[off[-1]:] == 9.0).all(), "rows of no group"
 
 
-@pytest.mark.parametrize("path", [7, 8, 9])
+@pytest.mark.parametrize("path", [7, 8, 9, 10])
 def test_grouped_many_tiles(path):
     """More tiles than a launch has blocks, of uneven groups."""
     d, K, N, E = dev(), 320, 2112, 12
@@ -432,7 +433,7 @@ def test_no_rows():
     assert L.llmint8_matmul_b128(q, s, wq, sw).shape == (0, 64)
 
 
-@pytest.mark.parametrize("path", [0, 1, 5, 8, 9])
+@pytest.mark.parametrize("path", [0, 1, 5, 8, 9, 10])
 @pytest.mark.parametrize("E", [3, 70])
 def test_grouped_bounds(E, path):
     """Offsets outside [0, M] and indices outside [0, T) count as the nearest bound."""
@@ -609,7 +610,7 @@ def test_large_activations():
     w, b = codes((N, K), 3), scales((1, 4), 4)
     rows = [slice(0, 300), slice((1 << 25) - 150, (1 << 25) + 150),
             slice((1 << 26) - 150, (1 << 26) + 150), slice(T - 300, T)]
-    for path in (0, 4, 6, 7, 8, 9):
+    for path in (0, 4, 6, 7, 8, 9, 10):
         say("large activations", path)
         out = L.llmint8.llmint8_matmul_b128_path(q, s, w, b, path=path, parts=1)
         for r in rows:
@@ -628,7 +629,7 @@ def test_large_activations_by_index():
     idx = torch.randint(T - (1 << 20), T, (M,), dtype=torch.int32, device="cuda", generator=g)
     idx[:4] = torch.tensor([T - 1, 0, 1 << 25, T - 2], dtype=torch.int32)
     off = torch.tensor([0, 300, 301, M], dtype=torch.int32, device="cuda")
-    for path in (0, 1, 6, 7, 8, 9):
+    for path in (0, 1, 6, 7, 8, 9, 10):
         say("large, by index", path)
         f = L.llmint8.llmint8_matmul_grouped_b128_path
         assert torch.equal(f(q, s, w, b, off, row_idx=idx, path=path),
@@ -640,7 +641,7 @@ def test_large_weights():
     K, N, E = 4160, (1 << 20) + 1024, 16
     w, b = codes((N, K), 1), scales((N // 128, 36), 2)
     be = scales((E, (N // E + 127) // 128, 36), 3)
-    for T, paths in ((5, (0, 1, 4)), (300, (0, 6, 7, 8, 9))):
+    for T, paths in ((5, (0, 1, 4)), (300, (0, 6, 7, 8, 9, 10))):
         q, s = codes((T, K), T), scales((T, 36), T + 1)
         off = torch.tensor([0] * (E - 1) + [T // 2, T], dtype=torch.int32, device="cuda")
         for path in paths:
