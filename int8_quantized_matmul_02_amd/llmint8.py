@@ -752,6 +752,23 @@ def llmint8_quantize_weight_b128(W_t, CB8=None, SB=None):
     """W_t: fp16 or bf16 [N,K], or [E,N,K] for the weights of E experts.  Returns (CB8 uint8 of
     the same shape, SB uint8 [ceil(N/128),pitch] or [E,ceil(N/128),pitch] scales of its
     128 x 128 blocks)."""
+    if CB8 is None and SB is None:
+        try:
+            dev, dt, shape = W_t.get_device(), W_t.dtype, W_t.shape
+            E, N, K = shape if len(shape) == 3 else (1, *shape)
+            if dt in _T16 and 0 <= dev == _current_device() and W_t.is_contiguous():
+                nb, p = (N + 127) // 128, (K + 511) // 512 * 4
+                c = _empty_like(W_t, dtype=_U8)
+                sb = (_matrix(nb, p, _U8, W_t.device) if len(shape) == 2 else
+                      _empty_strided((E, nb, p), (nb * p, p, 1), dtype=_U8, device=W_t.device))
+                rc = (_lib or _load()).llmint8_quantize_weight_b128(
+                    W_t.data_ptr(), _TYPES[dt], E, K, N, c.data_ptr(), sb.data_ptr(),
+                    _current_stream(dev))
+                if rc != LLMINT8_OK:
+                    raise LLMInt8Error("llmint8_quantize_weight_b128", rc)
+                return c, sb
+        except (AttributeError, TypeError, ValueError):
+            pass   # checked one by one below
     _arg(W_t, "W_t", _T16)
     if W_t.dim() not in (2, 3):
         raise ValueError("W_t must be [N,K] or [E,N,K], got shape %s" % (tuple(W_t.shape),))
