@@ -449,8 +449,8 @@ __global__ __launch_bounds__(C::kThreads) void k_b128_small(B128Args a)
 // stage at 2.37 GHz, 2048 of them MFMAs (64 of 32 cycles per SIMD); of the rest the
 // fragments' reads take 120, the scales' 60, barriers and loads 250.  With all
 // compute units busy the power limit holds the clock at 1.8 - 2.0 GHz: 4096 x 4096
-// x 16384 in 216 us = 2550 TFLOP/s, where the library's product of per-tensor scales
-// takes 227 on the same card; 8192^3 401 us (404).  A stage of 128 x 128 takes 960
+// x 16384 in 213 us = 2580 TFLOP/s, where the library's product of per-tensor scales
+// takes 225 on the same card; 8192^3 389 us (395).  A stage of 128 x 128 takes 960
 // cycles alone against 512 of MFMAs; two on each of all compute units take 0.95 us,
 // 0.25 of it for their loads (17 TB/s from L2).  Deeper rings (128 x 128 with 4
 // stages, 64 x 128 with 6) change nothing there.  Experts' weights come cold, in
